@@ -168,7 +168,7 @@ def prepare(case, seed):
         s["w_pre"] = (1.0 + _normal(gen, (H,), torch.float32, 0.1)).to(wd)
         s["w_post"] = (1.0 + _normal(gen, (H,), torch.float32, 0.1)).to(wd) if case["post"] else None
         s["gate"] = {"none": None, "channel": (0.4 + _normal(gen, (H,), torch.float32, 0.1)).to(wd),
-                     "token": (0.4 + _normal(gen, (T,), torch.float32, 0.1)).to(wd)}[case["gate"]]
+                     "token": (0.4 + _normal(gen, (T, 1), torch.float32, 0.1)).to(wd)}[case["gate"]]
         if op == "norm":
             s["x_out"], s["h"] = torch.zeros_like(s["x"]), torch.zeros_like(s["x"])
         else:
@@ -237,7 +237,7 @@ def _norm_forward(s):
     i1 = torch.rsqrt((y * y).mean(1, keepdim=True) + EPS) if c["post"] else None
     p = y * i1 if c["post"] else y
     r = p * s["w_post"].float() if c["post"] else y
-    gate = 1.0 if s["gate"] is None else s["gate"].float()[:, None] if c["gate"] == "token" else s["gate"].float()
+    gate = 1.0 if s["gate"] is None else s["gate"].float()
     xo = c["a"] * x + gate * r
     i2 = torch.rsqrt((xo * xo).mean(1, keepdim=True) + EPS)
     return i1, p, r, gate, xo, i2
@@ -257,7 +257,7 @@ def _plain(s):
         dr = dxo * gate
         out = dict(dx=(c["a"] * dxo).to(d), dw_pre=(dh * n).sum(0))
         if c["gate"] != "none":
-            out["dgate"] = (dxo * r).sum(1 if c["gate"] == "token" else 0)
+            out["dgate"] = (dxo * r).sum(1, keepdim=True) if c["gate"] == "token" else (dxo * r).sum(0)
         if c["post"]:
             out["dw_post"] = (dr * p).sum(0)
             dp = dr * s["w_post"].float()
@@ -433,8 +433,6 @@ def _exact_norm(s):
     w_pre = s["w_pre"].to(D)
     w_post = s["w_post"].to(D) if c["post"] else torch.ones(H, dtype=D, device="cuda")
     gate = torch.ones(1, dtype=D, device="cuda") if s["gate"] is None else s["gate"].to(D)
-    if c["gate"] == "token":
-        gate = gate.reshape(-1, 1)
     ry = torch.sqrt(y.square().sum(1, keepdim=True) / H + EPS) if c["post"] else torch.ones_like(y[:, :1])
     xo = x * c["a"] + y / ry * w_post * gate
     rx = torch.sqrt(xo.square().sum(1, keepdim=True) / H + EPS)
@@ -449,7 +447,7 @@ def _exact_norm(s):
     if c["gate"] == "channel":
         out["dgate"] = (dxo * (y / ry * w_post)).sum(0)
     elif c["gate"] == "token":
-        out["dgate"] = (dxo * (y / ry * w_post)).sum(1)
+        out["dgate"] = (dxo * (y / ry * w_post)).sum(1, keepdim=True)
     if c["post"]:
         out["dw_post"] = (branch * (y / ry)).sum(0)
         v = branch * w_post
