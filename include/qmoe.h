@@ -59,7 +59,8 @@ typedef enum moe_status {
 } moe_status;
 
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+/* MOE_F16 is taken by the expert products, block norms and SwiGLU only. */
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 typedef enum moe_path { MOE_PATH_AUTO = 0, MOE_PATH_DECODE = 1, MOE_PATH_PREFILL = 2, MOE_PATH_PREFILL_I8 = 3 } moe_path;
 typedef enum moe_format {
     MOE_FMT_Q8_0 = 0,
@@ -69,6 +70,11 @@ typedef enum moe_format {
     MOE_FMT_Q5K = 4,
     MOE_FMT_Q6K = 5
 } moe_format;
+
+/* How a call's rows are addressed from batch position q. */
+typedef enum moe_rows { MOE_ROWS_POSITION = 0, MOE_ROWS_PAIR = 1, MOE_ROWS_TOKEN = 2 } moe_rows;
+typedef enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate;
 
 /* Limits checked by the calls below. */
 #define MOE_MAX_EXPERTS 1024 /* E */
@@ -437,6 +443,147 @@ moe_status moe_expert_ffn_q4k_noalloc(const void* slot_pool, size_t slot_stride,
 moe_status moe_combine(const void* y_pairs, int y_pairs_dtype, const int32_t* topk_ids, const float* topk_w,
                        const int32_t* slot_of_expert, int E, int S, const float* y_shared, int T, int k, int H,
                        void* y, int y_dtype, void* stream);
+
+/* ------------------------------------------------------- expert products
+ * Matrix products grouped by expert over ragged batches, for experts kept
+ * unquantized (served in bf16 or fp16, or trained).  They read the batches
+ * of moe_build_expert_batches: slot s owns the batch positions q in
+ * [slot_offsets[s], slot_offsets[s+1]), position q is pair perm_pair[q], and
+ * pair p belongs to token p / k.  With w_s the [N, K] matrix of slot s
+ * (w + s * w_stride):
+ *
+ *   transpose 0:  y[iy(q), n] = sum over j < K of x[ix(q), j] * w_s[n, j]
+ *   transpose 1:  y[iy(q), j] = sum over n < N of x[ix(q), n] * w_s[n, j]
+ *                 (the gradient of the first form with respect to x)
+ *   act = MOE_ACT_SWIGLU (transpose 0): w_s holds N / 2 gate rows, then N / 2
+ *                 up rows, and y[iy(q), n] = silu(g_n) * u_n, n < N / 2.
+ *
+ * x          device, rows of K (transpose 1: N) elements, dtype MOE_BF16 or
+ *            MOE_F16.
+ * w          device, same dtype; w_stride bytes from one slot's matrix to the
+ *            next, a multiple of 16, at least N * K * 2.
+ * S          slots, 1..MOE_MAX_EXPERTS.
+ * N, K       multiples of 8 (MOE_ACT_SWIGLU: N a multiple of 16), N * K <=
+ *            2^30.
+ * slot_offsets  device, int32 [S + 1]; NULL with S = 1: slot 0 owns all R
+ *            positions (a dense product, e.g. a gate or a projection).
+ * R          batch positions (T * k), 0..2^24.  Positions at or behind
+ *            slot_offsets[S] belong to no slot.
+ * perm_pair  device, int32 [R]; may be NULL if x_rows and y_rows are both
+ *            MOE_ROWS_POSITION.
+ * k          pairs per token, 1..MOE_MAX_TOPK (used by MOE_ROWS_TOKEN).
+ * x_rows     how x is addressed: MOE_ROWS_POSITION: ix(q) = q (R rows),
+ *            MOE_ROWS_PAIR: ix(q) = perm_pair[q] (R rows), MOE_ROWS_TOKEN:
+ *            ix(q) = perm_pair[q] / k (R / k rows, rounded up).
+ * y_rows     how y is addressed: MOE_ROWS_POSITION or MOE_ROWS_PAIR, R rows.
+ * y          device, y_dtype: dtype or MOE_F32.  Rows of positions that no
+ *            slot owns are left as they were.
+ * Sums are fp32 over exact products; y is rounded once (SwiGLU: after it).
+ * x, w and y are 16-byte aligned; y overlaps neither x nor w.
+ *
+ * moe_expert_gemm_wgrad: the gradient with respect to the matrices,
+ *   dw_s[n, j] = sum over q of slot s of dy[iy(q), n] * x[ix(q), j]
+ * dy_rows, x_rows: any MOE_ROWS_*.  dw: device, [S, N, K], dw_dtype dtype or
+ * MOE_F32; every element is written (zeros for a slot that owns no position).
+ * ws: device workspace of moe_expert_gemm_wgrad_workspace_size (0 for
+ * arguments out of range), 16-byte aligned.
+ * The sums' order is fixed by the sizes and offsets, so equal calls give
+ * equal bits.
+ */
+moe_status moe_expert_gemm(const void* x, int dtype, const void* w, size_t w_stride, int S, int N, int K,
+                           int transpose, const int32_t* slot_offsets, int R, const int32_t* perm_pair, int k,
+                           int x_rows, int y_rows, int act, void* y, int y_dtype, void* stream);
+size_t moe_expert_gemm_wgrad_workspace_size(int S, int N, int K, int R);
+moe_status moe_expert_gemm_wgrad(const void* dy, const void* x, int dtype, int S, int N, int K,
+                                 const int32_t* slot_offsets, int R, const int32_t* perm_pair, int k, int dy_rows,
+                                 int x_rows, void* dw, int dw_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* -------------------------------------------- 4-bit group-scaled products
+ * moe_expert_gemm (transpose 0) with 4-bit weights, a scale and optionally a
+ * zero for each run of `group` inputs of a row:
+ *   w_s[n, j] = scales[s, n, j / group] * (code - zeros[s, n, j / group])
+ * For decode steps: every matrix of a slot with positions is read once for
+ * each 64 positions that the slot owns.
+ *
+ * q          device, [S, N, K / 2] bytes: element 2i of a row in the low
+ *            nibble of byte i, 2i + 1 in its high nibble (codes 0..15).
+ * scales     device, [S, N, K / group], scale_dtype: dtype or MOE_F32.
+ * zeros      device, uint8 [S, N, K / group], or NULL: every zero is 8.
+ * group      32, 64, 128 or 256; K a multiple of it.
+ * N          a multiple of 8 (MOE_ACT_SWIGLU: of 16); N * K <= 2^30.
+ * The other arguments as for moe_expert_gemm.  Codes and zeros enter exactly,
+ * sums are fp32, y is rounded once.  q is 16-byte aligned.
+ */
+moe_status moe_expert_gemv_w4(const void* x, int dtype, const void* q, const void* scales, int scale_dtype,
+                              const uint8_t* zeros, int group, int S, int N, int K, const int32_t* slot_offsets,
+                              int R, const int32_t* perm_pair, int k, int x_rows, int y_rows, int act, void* y,
+                              int y_dtype, void* stream);
+
+/* ------------------------------------------------------------ block norms
+ * What stands between the layer's output and the next block's input: the
+ * norm after the block, its gate, the residual sum and the norm before the
+ * next block, in one pass over the rows.  rms(v) = sqrt(mean(v^2) + eps):
+ *
+ *   r     = y / rms(y) * w_post        (y itself if w_post is NULL)
+ *   x_out = res_scale * x + gate * r   (gate 1 if NULL)
+ *   h     = x_out / rms(x_out) * w_pre
+ *
+ * With y = NULL it is the norm before a block alone: x_out = res_scale * x
+ * (w_post and gate must be NULL).  With w_pre = NULL there is no next norm
+ * (h must be NULL).
+ *
+ * x, x_out, h  device, [T, H], dtype MOE_F32, MOE_BF16 or MOE_F16.  x_out may
+ *            be NULL (only h is wanted), and may be x itself (in place).
+ * y          device, [T, H], y_dtype (any of the three), or NULL.
+ * w_post, w_pre  device, [H], w_dtype (any of the three), or NULL.
+ * gate       device, w_dtype, or NULL: gate_mode MOE_GATE_CHANNEL: [H],
+ *            MOE_GATE_TOKEN: [T], MOE_GATE_NONE: gate is NULL.
+ * H          a multiple of 8, 8..MOE_MAX_NORM_WIDTH.  T in 0..2^24.
+ * eps        >= 0, finite; res_scale finite.
+ * h is computed from the unrounded x_out; each output is rounded once.
+ *
+ * moe_block_norm_backward: the gradients of the same expressions for given
+ * dx_out and dh.  The row statistics are recomputed from x and y.
+ * dx_out, dh  device, [T, H], dtype; dx_out may be NULL (zero); dh is given iff
+ *            w_pre is.  At least one of them is given.
+ * dx, dy     device, [T, H], of dtype and y_dtype; dy iff y is given.
+ * dw_post, dgate, dw_pre
+ *            device, fp32, each iff its weight is given ([H]; dgate [T] for
+ *            MOE_GATE_TOKEN).  Overwritten.
+ * dx and dy may be dx_out and dh (in place) where the types agree.
+ * ws         device workspace of moe_block_norm_backward_workspace_size,
+ *            16-byte aligned.  Sums over rows are taken in an order fixed by
+ *            T and H (no atomics).
+ * All pointers to [T, H] and [H] arrays are 16-byte aligned.
+ */
+#define MOE_MAX_NORM_WIDTH 16384
+moe_status moe_block_norm(const void* x, int dtype, const void* y, int y_dtype, const void* w_post, const void* gate,
+                          int gate_mode, const void* w_pre, int w_dtype, int T, int H, float eps, float res_scale,
+                          void* x_out, void* h, void* stream);
+size_t moe_block_norm_backward_workspace_size(int T, int H);
+moe_status moe_block_norm_backward(const void* x, int dtype, const void* y, int y_dtype, const void* w_post,
+                                   const void* gate, int gate_mode, const void* w_pre, int w_dtype, int T, int H,
+                                   float eps, float res_scale, const void* dx_out, const void* dh, void* dx,
+                                   void* dy, float* dw_post, float* dgate, float* dw_pre, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* ----------------------------------------------------------------- SwiGLU
+ * h = silu(g) * u over rows [g | u], between two expert products that keep
+ * gu for the backward pass, and its gradient:
+ *   dg = dh * u * s * (1 + g * (1 - s)),  du = dh * g * s,  s = 1 / (1 + e^-g)
+ * gu, dgu    device, [R, 2 I], dtype MOE_F32, MOE_BF16 or MOE_F16.
+ * h, dh      device, [R, I].  In the backward call h is written again (for
+ *            the down product's weight gradient) unless it is NULL.
+ * I          a multiple of 8, up to 2^24; R in 0..2^24.
+ * slot_offsets, S  device, int32 [S + 1]: only rows below slot_offsets[S] are
+ *            computed, the others are left as they were; NULL with S = 0: all
+ *            R rows.
+ * dgu may be gu itself (in place).  16-byte aligned pointers.
+ */
+moe_status moe_swiglu(const void* gu, int dtype, int R, int I, const int32_t* slot_offsets, int S, void* h,
+                      void* stream);
+moe_status moe_swiglu_backward(const void* gu, const void* dh, int dtype, int R, int I, const int32_t* slot_offsets,
+                               int S, void* dgu, void* h, void* stream);
 
 /* ------------------------------------------------------------ stage timers
  * Diagnostics: one hipEvent pair per launch of a stage, attached to the

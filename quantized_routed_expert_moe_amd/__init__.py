@@ -86,13 +86,27 @@ def lib() -> ctypes.CDLL:
         L.moe_timer_read.argtypes = [i32, vp, i32, ctypes.POINTER(ctypes.c_int)]
         L.moe_hbm_read_probe.argtypes = [vp, sz, i32, i32, vp, ctypes.POINTER(ctypes.c_size_t), vp]
         L.moe_prefill_inner_probe.argtypes = [i32, i32, vp, sz, vp]
+        L.moe_expert_gemm.argtypes = [vp, i32, vp, sz, i32, i32, i32, i32, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp]
+        L.moe_expert_gemm_wgrad_workspace_size.argtypes = [i32] * 4
+        L.moe_expert_gemm_wgrad_workspace_size.restype = sz
+        L.moe_expert_gemm_wgrad.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, i32, i32, vp, i32, vp, sz, vp]
+        L.moe_expert_gemv_w4.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, i32, vp, i32, i32, i32, i32,
+                                         vp, i32, vp]
+        L.moe_block_norm.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, i32, i32, i32, f32, f32, vp, vp, vp]
+        L.moe_block_norm_backward_workspace_size.argtypes = [i32, i32]
+        L.moe_block_norm_backward_workspace_size.restype = sz
+        L.moe_block_norm_backward.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, i32, i32, i32, f32, f32] + [vp] * 8 + \
+            [sz, vp]
+        L.moe_swiglu.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp]
+        L.moe_swiglu_backward.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, vp, vp]
         for name in ("moe_route_topk", "moe_build_expert_batches", "moe_route_and_batch", "moe_count_routes",
                      "moe_pack_expert", "moe_unpack_expert", "moe_pack_q4k", "moe_pack_q8_0",
                      "moe_validate_slot_map", "moe_expert_ffn_q4k", "moe_expert_ffn_q8_0", "moe_expert_ffn_mxfp4",
                      "moe_expert_ffn_q3k_q4k", "moe_expert_ffn_q5k", "moe_expert_ffn_q6k", "moe_expert_ffn_q4k_noalloc",
                      "moe_combine", "moe_layer_decode",
                      "moe_timer_begin", "moe_timer_end", "moe_timer_read", "moe_hbm_read_probe",
-                     "moe_prefill_inner_probe"):
+                     "moe_prefill_inner_probe", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemv_w4",
+                     "moe_block_norm", "moe_block_norm_backward", "moe_swiglu", "moe_swiglu_backward"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -412,6 +426,246 @@ def moe_layer_decode(fmt: int, logits, x, k: int, score: int, renormalize: bool,
         _dev_or_mapped(host_expert, _i32(), "host_expert"), _dev_or_mapped(host_weight, _f32(), "host_weight"),
         _dev_or_mapped(host_count, _i32(), "host_count"), _dev(route_counts, _u32(), "route_counts"),
         _dev(y_pairs, _f32(), "y_pairs"), _dev(y, _f32(), "y"), _dev(ws, None, "ws"), ws_bytes, _stream(stream)))
+
+
+# ------------------------------------- expert products, block norms, SwiGLU
+# These calls take their sizes from the tensors' shapes and check every shape
+# that a kernel relies on.  All tensors live on the current device, on whose
+# current stream (or `stream`) the call is enqueued.
+
+MOE_F16 = 2
+MOE_ROWS_POSITION, MOE_ROWS_PAIR, MOE_ROWS_TOKEN = 0, 1, 2
+MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
+
+_torch = None
+_CODES = {}  # torch dtype -> moe_dtype
+_I32 = _U8 = None
+
+
+def _op_types() -> None:
+    global _torch, _I32, _U8
+    import torch
+    _CODES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
+    _I32, _U8 = torch.int32, torch.uint8
+    _torch = torch
+
+
+def _op_code(t, name: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, bfloat16 or float16")
+    return code
+
+
+def _op_ptrs(device: int, **tensors) -> list:
+    """Addresses of the given tensors (0 for None), each contiguous and on the device."""
+    out = []
+    for name, t in tensors.items():
+        if t is None:
+            out.append(0)
+            continue
+        if not isinstance(t, _torch.Tensor) or t.get_device() != device:
+            raise TypeError(f"{name} must be a tensor on the current device (cuda:{device})")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _op_device() -> int:
+    if _torch is None:
+        _op_types()
+    return _torch.cuda.current_device()
+
+
+def _op_stream(stream) -> int:
+    if stream is None:
+        stream = _torch.cuda.current_stream()
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _op_rows(slot_offsets, S: int, perm_pair, x, modes, k: int) -> int:
+    """Batch positions of a product: perm_pair's length, or x's rows without one."""
+    if slot_offsets is not None and (slot_offsets.dtype != _I32 or slot_offsets.shape != (S + 1,)):
+        raise ValueError(f"slot_offsets must be int32 [{S + 1}]")
+    if perm_pair is None:
+        if any(m != MOE_ROWS_POSITION for m in modes):
+            raise ValueError("the row modes need perm_pair")
+        return x.shape[0]
+    if perm_pair.dtype != _I32 or perm_pair.dim() != 1:
+        raise ValueError("perm_pair must be int32 [R]")
+    return perm_pair.shape[0]
+
+
+def _op_matrix(t, cols: int, R: int, mode: int, k: int, name: str) -> None:
+    need = -(-R // max(k, 1)) if mode == MOE_ROWS_TOKEN else R
+    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < need:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at least {need} rows of {cols}")
+
+
+def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: int = MOE_ROWS_POSITION,
+                    y_rows: int = MOE_ROWS_POSITION, transpose: bool = False, act: int = MOE_ACT_NONE, stream=None):
+    """y rows = x rows times their slot's matrix of w [S, N, K] (transposed unless `transpose`)."""
+    dev = _op_device()
+    if w.dim() != 3 or not w[0].is_contiguous():
+        raise ValueError("w must be [S, N, K] with contiguous matrices")
+    S, N, K = w.shape
+    wide_in, wide_out = (N, K) if transpose else (K, N // 2 if act else N)
+    R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
+    _op_matrix(x, wide_in, R, x_rows, k, "x")
+    _op_matrix(y, wide_out, R, y_rows, k, "y")
+    if w.dtype != x.dtype:
+        raise TypeError(f"w has dtype {w.dtype}, x {x.dtype}")
+    xp, wp, op, pp, yp = _op_ptrs(dev, x=x, w=w[0], slot_offsets=slot_offsets, perm_pair=perm_pair, y=y)
+    _check(lib().moe_expert_gemm(xp, _op_code(x, "x"), wp, 2 * (w.stride(0) if S > 1 else N * K), S, N, K,
+                                 int(bool(transpose)), op, R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"),
+                                 _op_stream(stream)))
+
+
+def moe_expert_gemm_wgrad_workspace_size(S: int, N: int, K: int, R: int) -> int:
+    return int(lib().moe_expert_gemm_wgrad_workspace_size(S, N, K, R))
+
+
+def moe_expert_gemm_wgrad(dy, x, slot_offsets, dw, perm_pair=None, k: int = 1, dy_rows: int = MOE_ROWS_POSITION,
+                          x_rows: int = MOE_ROWS_POSITION, ws=None, stream=None):
+    """dw [S, N, K] = per slot, the sum over its positions of dy row (outer) x row."""
+    dev = _op_device()
+    if dw.dim() != 3:
+        raise ValueError("dw must be [S, N, K]")
+    S, N, K = dw.shape
+    R = _op_rows(slot_offsets, S, perm_pair, x, (dy_rows, x_rows), k)
+    _op_matrix(dy, N, R, dy_rows, k, "dy")
+    _op_matrix(x, K, R, x_rows, k, "x")
+    if dy.dtype != x.dtype:
+        raise TypeError(f"dy has dtype {dy.dtype}, x {x.dtype}")
+    dp, xp, op, pp, wp, sp = _op_ptrs(dev, dy=dy, x=x, slot_offsets=slot_offsets, perm_pair=perm_pair, dw=dw, ws=ws)
+    _check(lib().moe_expert_gemm_wgrad(dp, xp, _op_code(x, "x"), S, N, K, op, R, pp, k, dy_rows, x_rows, wp,
+                                       _op_code(dw, "dw"), sp, 0 if ws is None else ws.numel() * ws.element_size(),
+                                       _op_stream(stream)))
+
+
+def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pair=None, k: int = 1,
+                       x_rows: int = MOE_ROWS_POSITION, y_rows: int = MOE_ROWS_POSITION, act: int = MOE_ACT_NONE,
+                       stream=None):
+    """y rows = x rows times their slot's 4-bit matrix: codes q [S, N, K / 2], scales (and zeros) [S, N, K / group]."""
+    dev = _op_device()
+    if q.dim() != 3 or q.dtype != _U8:
+        raise ValueError("q must be uint8 [S, N, K / 2]")
+    S, N, K = q.shape[0], q.shape[1], 2 * q.shape[2]
+    if group < 1 or scales.shape != (S, N, K // group):
+        raise ValueError(f"scales have shape {tuple(scales.shape)}, expected [{S}, {N}, K / group]")
+    if zeros is not None and (zeros.dtype != _U8 or zeros.shape != scales.shape):
+        raise ValueError("zeros must be uint8 with the shape of scales")
+    R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
+    _op_matrix(x, K, R, x_rows, k, "x")
+    _op_matrix(y, N // 2 if act else N, R, y_rows, k, "y")
+    xp, qp, sp, zp, op, pp, yp = _op_ptrs(dev, x=x, q=q, scales=scales, zeros=zeros, slot_offsets=slot_offsets,
+                                          perm_pair=perm_pair, y=y)
+    _check(lib().moe_expert_gemv_w4(xp, _op_code(x, "x"), qp, sp, _op_code(scales, "scales"), zp, group, S, N, K, op,
+                                    R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"), _op_stream(stream)))
+
+
+def _norm_shapes(x, y, w_post, gate, w_pre) -> tuple:
+    """(T, H, gate mode, weight type) of a block norm's tensors."""
+    if x.dim() != 2 or (y is not None and y.shape != x.shape):
+        raise ValueError("x and y must be [T, H] of one shape")
+    T, H = x.shape
+    w_dtype = None
+    for name, w in (("w_post", w_post), ("w_pre", w_pre), ("gate", gate)):
+        if w is None:
+            continue
+        if w_dtype is None:
+            w_dtype = w.dtype
+        if w.dtype != w_dtype:
+            raise TypeError("w_post, gate and w_pre must have one dtype")
+        if name != "gate" and w.shape != (H,):
+            raise ValueError(f"{name} must be [{H}]")
+    mode = MOE_GATE_NONE
+    if gate is not None:
+        if gate.shape == (H,):
+            mode = MOE_GATE_CHANNEL
+        elif gate.shape == (T, 1):
+            mode = MOE_GATE_TOKEN
+        else:
+            raise ValueError(f"gate has shape {tuple(gate.shape)}, expected [{H}] (a channel's) or [{T}, 1] (a token's)")
+    first = w_post if w_post is not None else w_pre if w_pre is not None else gate
+    return T, H, mode, MOE_F32 if first is None else _op_code(first, "weights")
+
+
+def _norm_like(t, want, name: str) -> None:
+    if t is not None and (t.shape != want.shape or t.dtype != want.dtype):
+        raise ValueError(f"{name} must have shape {tuple(want.shape)} and dtype {want.dtype}")
+
+
+def moe_block_norm(x, y, w_post, gate, w_pre, x_out, h, eps: float, res_scale: float = 1.0, stream=None):
+    """x_out = res_scale x + gate norm(y) w_post and h = norm(x_out) w_pre in one pass over the rows.  gate: [H] (one
+    for each channel), [T, 1] (one for each token) or None; y, w_post, w_pre, x_out and h may be None."""
+    dev = _op_device()
+    T, H, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
+    _norm_like(x_out, x, "x_out")
+    _norm_like(h, x, "h")
+    xp, yp, wp, gp, np_, op, hp = _op_ptrs(dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, x_out=x_out, h=h)
+    _check(lib().moe_block_norm(xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_,
+                                w_code, T, H, eps, res_scale, op, hp, _op_stream(stream)))
+
+
+def moe_block_norm_backward_workspace_size(T: int, H: int) -> int:
+    return int(lib().moe_block_norm_backward_workspace_size(T, H))
+
+
+def moe_block_norm_backward(x, y, w_post, gate, w_pre, dx_out, dh, dx, dy, dw_post, dgate, dw_pre, eps: float,
+                            res_scale: float = 1.0, ws=None, stream=None):
+    """The gradients of moe_block_norm's outputs with respect to x, y and the channel vectors (fp32)."""
+    dev = _op_device()
+    T, H, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
+    _norm_like(dx_out, x, "dx_out")
+    _norm_like(dh, x, "dh")
+    _norm_like(dx, x, "dx")
+    if y is not None:
+        _norm_like(dy, y, "dy")
+    for name, d, w in (("dw_post", dw_post, w_post), ("dgate", dgate, gate), ("dw_pre", dw_pre, w_pre)):
+        if (d is None) != (w is None) or (d is not None and (d.dtype != _torch.float32 or d.shape != w.shape)):
+            raise ValueError(f"{name} must be float32 with the shape of its weight, and None without one")
+    xp, yp, wp, gp, np_, op, hp, dxp, dyp, d0, d1, d2, sp = _op_ptrs(
+        dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, dx_out=dx_out, dh=dh, dx=dx, dy=dy, dw_post=dw_post,
+        dgate=dgate, dw_pre=dw_pre, ws=ws)
+    _check(lib().moe_block_norm_backward(
+        xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_, w_code, T, H, eps,
+        res_scale, op, hp, dxp, dyp, d0, d1, d2, sp, 0 if ws is None else ws.numel() * ws.element_size(),
+        _op_stream(stream)))
+
+
+def _swiglu_shapes(gu, slot_offsets, **halves) -> tuple:
+    if gu.dim() != 2 or gu.shape[1] % 2:
+        raise ValueError("gu must be [R, 2 I]")
+    R, I = gu.shape[0], gu.shape[1] // 2
+    for name, t in halves.items():
+        if t is not None and (t.shape != (R, I) or t.dtype != gu.dtype):
+            raise ValueError(f"{name} must be [{R}, {I}] of dtype {gu.dtype}")
+    S = 0
+    if slot_offsets is not None:
+        if slot_offsets.dtype != _I32 or slot_offsets.dim() != 1:
+            raise ValueError("slot_offsets must be int32 [S + 1]")
+        S = slot_offsets.shape[0] - 1
+    return R, I, S
+
+
+def moe_swiglu(gu, h, slot_offsets=None, stream=None):
+    """h [R, I] = silu(g) u of rows gu = [g | u]; with slot_offsets only the rows that a slot owns."""
+    dev = _op_device()
+    R, I, S = _swiglu_shapes(gu, slot_offsets, h=h)
+    gp, op, hp = _op_ptrs(dev, gu=gu, slot_offsets=slot_offsets, h=h)
+    _check(lib().moe_swiglu(gp, _op_code(gu, "gu"), R, I, op, S, hp, _op_stream(stream)))
+
+
+def moe_swiglu_backward(gu, dh, dgu, h=None, slot_offsets=None, stream=None):
+    """dgu [R, 2 I] for given dh [R, I]; h is written again unless None."""
+    dev = _op_device()
+    R, I, S = _swiglu_shapes(gu, slot_offsets, dh=dh, h=h)
+    _norm_like(dgu, gu, "dgu")
+    gp, dp, op, up, hp = _op_ptrs(dev, gu=gu, dh=dh, slot_offsets=slot_offsets, dgu=dgu, h=h)
+    _check(lib().moe_swiglu_backward(gp, dp, _op_code(gu, "gu"), R, I, op, S, up, hp, _op_stream(stream)))
 
 
 # ------------------------------------------------------------ host leg

@@ -14,6 +14,7 @@
 #include "qmoe.h"
 #include "qmoe_internal.h"
 #include "prefill_i8.h"
+#include "expert_ops.h"
 
 namespace {
 
@@ -680,6 +681,11 @@ moe_status scratch_address(void** out) {
 }  // namespace
 
 namespace qmoe {
+
+moe_status set_error(moe_status st, const char* text) {
+    g_error = text;
+    return st;
+}
 
 StageEvents timer_events(int stage) {
     StageTimer& t = g_timer[stage];

@@ -1,0 +1,60 @@
+// SwiGLU between two expert products and its gradient: elementwise over rows
+// [g | u] of 2 I elements, bound by HBM (3 and 6 element-sized streams).
+// A thread owns eight consecutive features of a row: 16-byte accesses for
+// the 16-bit types.
+#include "expert_ops.h"
+
+namespace qmoe {
+
+template <int DT, bool BACKWARD>
+__global__ __launch_bounds__(256) void swiglu_kernel(const void* gu, const void* dh, int R, int I,
+                                                     const int32_t* __restrict__ offsets, int S, void* dgu, void* h) {
+    const int rows = offsets ? min(max(offsets[S], 0), R) : R;
+    const uint32_t per_row = I / 8;
+    const uint64_t total = (uint64_t)rows * per_row, step = (uint64_t)gridDim.x * 256;
+    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += step) {
+        const uint64_t row = i / per_row;
+        const size_t c = (size_t)(i - row * per_row) * 8, base = row * 2 * I + c, out = row * I + c;
+        float g[8], u[8], d[8], hv[8], dg[8], du[8];
+        load_vec8<DT>(gu, base, g);
+        load_vec8<DT>(gu, base + I, u);
+        if (BACKWARD) load_vec8<DT>(dh, out, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float s = sigmoid_f32(g[j]);
+            hv[j] = g[j] * s * u[j];
+            if (BACKWARD) {
+                dg[j] = d[j] * u[j] * s * (1.0f + g[j] * (1.0f - s));
+                du[j] = d[j] * g[j] * s;
+            }
+        }
+        if (BACKWARD) {
+            store_vec8<DT>(dgu, base, dg);
+            store_vec8<DT>(dgu, base + I, du);
+        }
+        if (h) store_vec8<DT>(h, out, hv);
+    }
+}
+
+template <bool BACKWARD>
+static hipError_t launch(const SwigluArgs& a, hipStream_t s) {
+    const uint64_t n = (uint64_t)a.R * (a.I / 8);
+    if (n == 0) return hipSuccess;
+    const dim3 grid((uint32_t)((n + 255) / 256 < 8192 ? (n + 255) / 256 : 8192));
+    switch (a.dtype) {
+        case MOE_F32:
+            swiglu_kernel<MOE_F32, BACKWARD><<<grid, 256, 0, s>>>(a.gu, a.dh, a.R, a.I, a.offsets, a.S, a.dgu, a.h);
+            break;
+        case MOE_BF16:
+            swiglu_kernel<MOE_BF16, BACKWARD><<<grid, 256, 0, s>>>(a.gu, a.dh, a.R, a.I, a.offsets, a.S, a.dgu, a.h);
+            break;
+        default:
+            swiglu_kernel<MOE_F16, BACKWARD><<<grid, 256, 0, s>>>(a.gu, a.dh, a.R, a.I, a.offsets, a.S, a.dgu, a.h);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) { return launch<false>(a, s); }
+hipError_t launch_swiglu_backward(const SwigluArgs& a, hipStream_t s) { return launch<true>(a, s); }
+
+}  // namespace qmoe
