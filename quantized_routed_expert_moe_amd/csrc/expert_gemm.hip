@@ -1,6 +1,6 @@
 // Matrix products grouped by expert over ragged batches, and the weight
 // gradient: the simple form, one output element per thread.
-#include "expert_ops.h"
+#include "expert_stream.h"
 
 namespace qmoe {
 
@@ -61,6 +61,12 @@ __global__ __launch_bounds__(256) void expert_wgrad_simple(const ExpertWgradArgs
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
+    const int slots = a.rows.offsets && a.rows.S < a.rows.R ? a.rows.S : a.rows.offsets ? a.rows.R : 1;
+    if (!a.transpose && a.rows.R <= 32 * slots) {
+        const StreamArgs t{a.x, a.w, a.w_stride, nullptr, nullptr, 0, 0, a.N, a.K, a.rows, a.x_rows, a.y_rows, a.y,
+                           a.y_dtype == MOE_F32};
+        return a.dtype == MOE_BF16 ? launch_stream_bf16(t, 0, a.act, s) : launch_stream_f16(t, 0, a.act, s);
+    }
     const int out = a.transpose ? a.K : a.act ? a.N / 2 : a.N;
     const int gy = a.rows.R < 32768 ? a.rows.R : 32768;
     const dim3 grid((out + 255) / 256, gy, (a.rows.R + gy - 1) / gy);

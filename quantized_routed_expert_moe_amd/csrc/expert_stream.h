@@ -1,0 +1,293 @@
+// Expert products with few rows a slot: the weights are streamed once and
+// every element goes from its load straight into a matrix instruction.
+//
+// Bound by HBM: a decode step reads each used matrix once (N K / 2 bytes of
+// codes or 2 N K of 16-bit weights) for a handful of rows.  A workgroup owns
+// 16 NT columns of one slot's product, its waves split K in segments of 256,
+// and one LDS sum joins them: no second launch, no atomics, a fixed order.
+//
+// v_mfma_f32_16x16x32 takes the rows of x as its A operand (up to 16 a
+// block, MB blocks) and 16 rows of w as its B operand: lane l holds eight
+// inputs of weight row l % 16, which is what a 16-byte load along the row
+// gives, so the weights pass through no LDS and need no shuffle.  Padding one
+// row to 16 costs matrix-core time that a bandwidth-bound kernel has to
+// spare, and spares the vector units the products, which for 4-bit weights
+// they need for the dequantization.
+//
+// 4-bit weights: a byte 0..15 is the fp8 (e4m3) code of q / 512, so one
+// v_cvt_scalef32_pk_{bf16,f16}_fp8 with scale 512 turns two codes into two
+// exact 16-bit values: 7 instructions for 8 weights.  It yields elements
+// 0 2 4 6 1 3 5 7 of a word; the x fragments are put in that order (four byte
+// permutes for 16 rows x 8 inputs), the sum does not care.  With zero points
+//   sum_j s (q_j - z) x_j = s (sum_j q_j x_j - z sum_j x_j),
+// where sum_j x_j comes from one more matrix instruction against ones, in
+// the accumulator's own layout.  PER matrix instructions (32 inputs each)
+// share a group; groups of less than 128 inputs need each instruction's 32
+// inputs from one run, which a 4 x 4 transposition of words between the
+// lanes' quarters gives (v_permlane16/32_swap).
+#pragma once
+#include "expert_ops.h"
+
+namespace qmoe {
+
+struct StreamArgs {
+    const void* x;
+    const void* w;      // 16-bit weights or code bytes
+    size_t w_stride;    // bytes from slot to slot
+    const void* scales;
+    const uint8_t* zeros;
+    int scale_f32, group_shift;
+    int N, K;
+    RowMap rows;
+    int x_rows, y_rows;
+    void* y;
+    int y_f32;
+};
+
+constexpr int kSegment = 256;  // inputs a wave takes at a time
+constexpr int kStreamWaves = 8;
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+    if constexpr (DT == MOE_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                      0);
+}
+
+// Eight codes of a word -> elements 0 2 4 6 1 3 5 7 as exact 16-bit values.
+template <int DT>
+__device__ __forceinline__ uint4 codes_frag(uint32_t w) {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    uint4 f;
+    if constexpr (DT == MOE_BF16) {
+        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
+        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
+        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
+        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
+    } else {
+        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false));
+        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true));
+        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false));
+        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true));
+    }
+    return f;
+}
+
+// Eight 16-bit values in the order of codes_frag.
+__device__ __forceinline__ uint4 codes_order(uint4 v) {
+    return make_uint4(__builtin_amdgcn_perm(v.y, v.x, 0x05040100u), __builtin_amdgcn_perm(v.w, v.z, 0x05040100u),
+                      __builtin_amdgcn_perm(v.y, v.x, 0x07060302u), __builtin_amdgcn_perm(v.w, v.z, 0x07060302u));
+}
+
+// Word j of lane quarter c <- word c of quarter j (quarter = lane / 16).
+__device__ __forceinline__ uint4 transpose_quarters(uint4 v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return make_uint4(c[0], c[1], d[0], d[1]);
+}
+
+// Slot of index i: with fewer positions than slots the i-th slot that owns
+// one (found by a ballot scan), otherwise slot i.  -1: none.
+__device__ __forceinline__ int stream_slot(const RowMap& m, int i) {
+    if (!m.offsets || m.R >= m.S) return i;
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int s0 = 0; s0 < m.S; s0 += 64) {
+        const int s = s0 + lane;
+        const bool owns = s < m.S && slot_range(m, s).y > 0;
+        uint64_t mask = __ballot(owns);
+        const int n = __popcll(mask);
+        if (i < before + n) {
+            for (int k = i - before; k > 0; --k) mask &= mask - 1;
+            return s0 + __ffsll((unsigned long long)mask) - 1;
+        }
+        before += n;
+    }
+    return -1;
+}
+
+// WT 0: 16-bit weights, 1: 4-bit.  SWI: tile 0 holds gate rows, tile 1 the up
+// rows of the same 16 features (NT = 2).
+template <int WT, int DT, int NT, int MB, int PER, bool SWI>
+__global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const StreamArgs a) {
+    typedef typename DType<DT>::type E;
+    extern __shared__ float red[];  // [waves][NT][MB][64][4]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int col = lane & 15, c = lane >> 4;
+    const int slot = __builtin_amdgcn_readfirstlane(stream_slot(a.rows, blockIdx.y));
+    if (slot < 0) return;
+    const int2 r = slot_range(a.rows, slot);
+    const int N = a.N, K = a.K, half = N / 2, width = SWI ? half : N;
+    const int n0 = blockIdx.x * (SWI ? 16 : 16 * NT);
+    const uint8_t* w = static_cast<const uint8_t*>(a.w) + (size_t)slot * a.w_stride;
+    const uint8_t* wp[NT];
+    size_t sp[NT];  // first scale of the lane's weight row
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int n = SWI ? min(n0 + col, half - 1) + t * half : min(n0 + 16 * t + col, N - 1);
+        wp[t] = w + (WT ? (size_t)n * (K / 2) : (size_t)n * K * 2);
+        sp[t] = WT ? ((size_t)slot * N + n) * (K >> a.group_shift) : 0;
+    }
+    for (int rb = 0; rb < r.y; rb += 16 * MB) {
+        const int nr = min(r.y - rb, 16 * MB);
+        const E* xp[MB];
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            const int i = min(16 * m + col, nr - 1);
+            xp[m] = static_cast<const E*>(a.x) + (size_t)row_of(a.rows, a.x_rows, r.x + rb + i) * K;
+        }
+        f32x4 tot[NT][MB] = {};
+        for (int k0 = wave * kSegment; k0 < K; k0 += waves * kSegment) {
+            constexpr int LD = WT ? 2 : 8;  // 16-byte weight loads a tile
+            uint4 wv[NT][LD], xv[MB][8];
+#pragma unroll
+            for (int i = 0; i < LD; ++i) {
+                const int k = WT ? k0 + 128 * i + 32 * c : k0 + 32 * i + 8 * c;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    wv[t][i] = k < K ? *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2)) : make_uint4(0, 0, 0, 0);
+            }
+            constexpr int SG = WT ? 8 / PER : 1;  // groups of the segment
+            float sc[NT][SG], zr[NT][SG];
+            if constexpr (WT) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int g = 0; g < SG; ++g) {
+                        const int k = k0 + 32 * PER * g;
+                        const size_t at = sp[t] + (min(k, K - 1) >> a.group_shift);
+                        const float s = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
+                                                    : (float)static_cast<const E*>(a.scales)[at];
+                        sc[t][g] = k < K ? s : 0.0f;
+                        zr[t][g] = a.zeros ? (float)a.zeros[at] : 8.0f;
+                    }
+            }
+            // x fragments: instruction i takes the inputs that the weights' words hold
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int k = WT && PER == 4 ? k0 + 128 * (i / 4) + 32 * c + 8 * (i % 4) : k0 + 32 * i + 8 * c;
+                    const bool in = k < K && 16 * m + col < nr;
+                    xv[m][i] = in ? *reinterpret_cast<const uint4*>(xp[m] + k) : make_uint4(0, 0, 0, 0);
+                }
+            if constexpr (WT) {
+                const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
+                const uint4 ones = make_uint4(one, one, one, one);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (PER < 4) wv[t][i] = transpose_quarters(wv[t][i]);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) xv[m][i] = codes_order(xv[m][i]);
+#pragma unroll
+                for (int g = 0; g < SG; ++g) {
+                    f32x4 acc[NT][MB] = {}, sx[MB] = {};
+#pragma unroll
+                    for (int p = 0; p < PER; ++p) {
+                        const int i = g * PER + p;
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const uint4 v = wv[t][i / 4];
+                            const uint4 f = codes_frag<DT>(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+#pragma unroll
+                            for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xv[m][i], f, acc[t][m]);
+                        }
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) sx[m] = mfma16<DT>(xv[m][i], ones, sx[m]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                tot[t][m][e] = fmaf(sc[t][g], fmaf(-zr[t][g], sx[m][e], acc[t][m][e]), tot[t][m][e]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][i], wv[t][i], tot[t][m]);
+            }
+        }
+        // join the waves' parts in wave order; element (row, col) of a block
+        // sits at lane 16 (row / 4) + col, component row % 4
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                *reinterpret_cast<f32x4*>(red + (((wave * NT + t) * MB + m) * 64 + lane) * 4) = tot[t][m];
+        __syncthreads();
+        constexpr int TILES = SWI ? 1 : NT;
+        for (int o = threadIdx.x; o < TILES * nr * 16; o += blockDim.x) {
+            const int cc = o & 15, row = (o >> 4) % nr, t = (o >> 4) / nr;
+            const int at = ((row >> 4) * 64 + ((row & 15) >> 2) * 16 + cc) * 4 + (row & 3);
+            float v[2] = {0.0f, 0.0f};
+            for (int u = 0; u < waves; ++u) {
+                v[0] += red[(u * NT + t) * MB * 256 + at];
+                if (SWI) v[1] += red[(u * NT + 1) * MB * 256 + at];
+            }
+            const int n = n0 + 16 * t + cc;
+            if (n >= width) continue;
+            if (SWI) v[0] = v[0] * sigmoid_f32(v[0]) * v[1];
+            const size_t out = (size_t)row_of(a.rows, a.y_rows, r.x + rb + row) * width + n;
+            if (a.y_f32) static_cast<float*>(a.y)[out] = v[0];
+            else static_cast<E*>(a.y)[out] = (E)v[0];
+        }
+        __syncthreads();
+    }
+}
+
+template <int WT, int DT, int NT, int PER, bool SWI>
+static hipError_t stream_launch_rows(const StreamArgs& a, int mb, dim3 grid, int waves, hipStream_t s) {
+    const size_t lds = (size_t)waves * NT * mb * 1024;
+    if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else if (mb == 2) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    return hipGetLastError();
+}
+
+template <int WT, int DT, int PER>
+static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
+    if (a.rows.R == 0) return hipSuccess;
+    const int slots = a.rows.offsets ? (a.rows.R < a.rows.S ? a.rows.R : a.rows.S) : 1;
+    const int mean = (a.rows.R + slots - 1) / slots;
+    // Rows a pass: twice the mean and more, so that a slot above it still
+    // takes one pass over its weights.
+    const int mb = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
+    const int segs = (a.K + kSegment - 1) / kSegment, turns = (segs + kStreamWaves - 1) / kStreamWaves;
+    const int waves = (segs + turns - 1) / turns;
+    const int width = act ? a.N / 2 : a.N;
+    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(a, mb, dim3((width + 15) / 16, slots), waves, s);
+    const int tiles = (width + 15) / 16;
+    // one tile a workgroup while that leaves CUs without one
+    if ((long long)tiles * slots <= 512)
+        return stream_launch_rows<WT, DT, 1, PER, false>(a, mb, dim3(tiles, slots), waves, s);
+    return stream_launch_rows<WT, DT, 2, PER, false>(a, mb, dim3((tiles + 1) / 2, slots), waves, s);
+}
+
+template <int DT>
+static hipError_t stream_launch_type(const StreamArgs& a, int w4, int act, hipStream_t s) {
+    if (!w4) return stream_launch<0, DT, 4>(a, act, s);
+    switch (a.group_shift) {
+        case 5: return stream_launch<1, DT, 1>(a, act, s);
+        case 6: return stream_launch<1, DT, 2>(a, act, s);
+        default: return stream_launch<1, DT, 4>(a, act, s);
+    }
+}
+
+hipError_t launch_stream_bf16(const StreamArgs& a, int w4, int act, hipStream_t s);
+hipError_t launch_stream_f16(const StreamArgs& a, int w4, int act, hipStream_t s);
+
+}  // namespace qmoe
