@@ -503,13 +503,13 @@ moe_status moe_expert_gemm_wgrad(const void* dy, const void* x, int dtype, int S
  * zero for each run of `group` inputs of a row:
  *   w_s[n, j] = scales[s, n, j / group] * (code - zeros[s, n, j / group])
  * For decode steps: every matrix of a slot with positions is read once for
- * each 64 positions that the slot owns.
+ * each 64 positions (groups of 32: 32 positions) that the slot owns.
  *
  * q          device, [S, N, K / 2] bytes: element 2i of a row in the low
  *            nibble of byte i, 2i + 1 in its high nibble (codes 0..15).
  * scales     device, [S, N, K / group], scale_dtype: dtype or MOE_F32.
  * zeros      device, uint8 [S, N, K / group], or NULL: every zero is 8.
- * group      32, 64, 128 or 256; K a multiple of it.
+ * group      32, 64 or 128; K a multiple of it.
  * N          a multiple of 8 (MOE_ACT_SWIGLU: of 16); N * K <= 2^30.
  * The other arguments as for moe_expert_gemm.  Codes and zeros enter exactly,
  * sums are fp32, y is rounded once.  q is 16-byte aligned.

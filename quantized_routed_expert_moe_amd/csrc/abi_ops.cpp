@@ -113,8 +113,8 @@ moe_status moe_expert_gemv_w4(const void* x, int dtype, const void* q, const voi
                               int y_dtype, void* stream) {
     moe_status st = check_product(dtype, S, N, K, slot_offsets, R, perm_pair, k, x_rows, y_rows, act);
     if (st != MOE_OK) return st;
-    if (group != 32 && group != 64 && group != 128 && group != 256)
-        return fail(MOE_ERR_UNSUPPORTED, "group = %d is not 32, 64, 128 or 256", group);
+    if (group != 32 && group != 64 && group != 128)
+        return fail(MOE_ERR_UNSUPPORTED, "group = %d is not 32, 64 or 128", group);
     if (K % group) return fail(MOE_ERR_UNSUPPORTED, "K = %d is not a multiple of the group (%d)", K, group);
     if (y_rows == MOE_ROWS_TOKEN) return fail(MOE_ERR_INVALID_ARGUMENT, "y_rows cannot be MOE_ROWS_TOKEN");
     if ((st = check_output(dtype, scale_dtype, "scale")) != MOE_OK) return st;

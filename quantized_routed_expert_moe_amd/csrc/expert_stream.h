@@ -26,6 +26,8 @@
 // inputs from one run, which a 4 x 4 transposition of words between the
 // lanes' quarters gives (v_permlane16/32_swap).
 #pragma once
+#include <type_traits>
+
 #include "expert_ops.h"
 
 namespace qmoe {
@@ -97,16 +99,23 @@ __device__ __forceinline__ int stream_slot(const RowMap& m, int i) {
     if (!m.offsets || m.R >= m.S) return i;
     const int lane = threadIdx.x & 63;
     int before = 0;
-    for (int s0 = 0; s0 < m.S; s0 += 64) {
-        const int s = s0 + lane;
-        const bool owns = s < m.S && slot_range(m, s).y > 0;
-        uint64_t mask = __ballot(owns);
-        const int n = __popcll(mask);
-        if (i < before + n) {
-            for (int k = i - before; k > 0; --k) mask &= mask - 1;
-            return s0 + __ffsll((unsigned long long)mask) - 1;
+    for (int s0 = 0; s0 < m.S; s0 += 256) {
+        bool owns[4];  // four loads in flight, then the ballots
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = s0 + 64 * j + lane;
+            owns[j] = slot_range(m, min(s, m.S - 1)).y > 0 && s < m.S;
         }
-        before += n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint64_t mask = __ballot(owns[j]);
+            const int n = __popcll(mask);
+            if (i < before + n) {
+                for (int k = i - before; k > 0; --k) mask &= mask - 1;
+                return s0 + 64 * j + __ffsll((unsigned long long)mask) - 1;
+            }
+            before += n;
+        }
     }
     return -1;
 }
@@ -117,7 +126,7 @@ template <int WT, int DT, int NT, int MB, int PER, bool SWI>
 __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const StreamArgs a) {
     typedef typename DType<DT>::type E;
     extern __shared__ float red[];  // [waves][NT][MB][64][4]
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int col = lane & 15, c = lane >> 4;
     const int slot = __builtin_amdgcn_readfirstlane(stream_slot(a.rows, blockIdx.y));
     if (slot < 0) return;
@@ -142,85 +151,145 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
             xp[m] = static_cast<const E*>(a.x) + (size_t)row_of(a.rows, a.x_rows, r.x + rb + i) * K;
         }
         f32x4 tot[NT][MB] = {};
-        for (int k0 = wave * kSegment; k0 < K; k0 += waves * kSegment) {
-            constexpr int LD = WT ? 2 : 8;  // 16-byte weight loads a tile
-            uint4 wv[NT][LD], xv[MB][8];
+        // One segment of 256 inputs.  Every load is issued before the first
+        // use; only the last segment of a row may be cut, and only its copy of
+        // the code tests inputs (one body for both would merge their registers
+        // at the price of a wait behind each load).
+        auto segment = [&](int k0, auto cut_tag) {
+            constexpr bool CUT = decltype(cut_tag)::value;
+            constexpr int LD = WT ? 2 : 8;          // 16-byte weight loads a tile
+            constexpr int SG = WT ? 8 / PER : 2;    // groups of the segment
+            constexpr int XI = MB == 4 ? 4 : 8;     // x instructions held at a time: 64 rows of eight would spill
+            typedef uint32_t s16v __attribute__((ext_vector_type(SG / 2)));
+            typedef uint32_t s32v __attribute__((ext_vector_type(SG)));
+            uint4 wv[NT][LD], xv[MB][XI];
+            s16v s16[NT];
+            s32v s32[NT];
+            uint64_t zraw[NT];
+            if constexpr (WT) {
+                // A row's groups of the segment lie side by side: one load of up
+                // to 16 bytes (2- or 1-byte aligned), since single values cost
+                // the address unit a lane at a time.  They come first: the branch
+                // on their type costs a wait for what is in flight.
+                auto at = [&](int t, int g) { return sp[t] + (min(k0 + 32 * PER * g, K - 1) >> a.group_shift); };
+                if (a.scale_f32) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t* p = static_cast<const uint32_t*>(a.scales);
+                        if (!CUT) __builtin_memcpy(&s32[t], p + at(t, 0), 4 * SG);
+                        else
+#pragma unroll
+                            for (int g = 0; g < SG; ++g) s32[t][g] = p[at(t, g)];
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint16_t* p = static_cast<const uint16_t*>(a.scales);
+                        if (!CUT) __builtin_memcpy(&s16[t], p + at(t, 0), 2 * SG);
+                        else
+#pragma unroll
+                            for (int g = 0; g < SG; g += 2) s16[t][g / 2] = p[at(t, g)] | (uint32_t)p[at(t, g + 1)] << 16;
+                    }
+                }
+                if (a.zeros) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        zraw[t] = 0;
+                        if (!CUT) __builtin_memcpy(&zraw[t], a.zeros + at(t, 0), SG);
+                        else
+#pragma unroll
+                            for (int g = 0; g < SG; ++g) zraw[t] |= (uint64_t)a.zeros[at(t, g)] << (8 * g);
+                    }
+                }
+            }
 #pragma unroll
             for (int i = 0; i < LD; ++i) {
                 const int k = WT ? k0 + 128 * i + 32 * c : k0 + 32 * i + 8 * c;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    wv[t][i] = k < K ? *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2)) : make_uint4(0, 0, 0, 0);
-            }
-            constexpr int SG = WT ? 8 / PER : 1;  // groups of the segment
-            float sc[NT][SG], zr[NT][SG];
-            if constexpr (WT) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int g = 0; g < SG; ++g) {
-                        const int k = k0 + 32 * PER * g;
-                        const size_t at = sp[t] + (min(k, K - 1) >> a.group_shift);
-                        const float s = a.scale_f32 ? static_cast<const float*>(a.scales)[at]
-                                                    : (float)static_cast<const E*>(a.scales)[at];
-                        sc[t][g] = k < K ? s : 0.0f;
-                        zr[t][g] = a.zeros ? (float)a.zeros[at] : 8.0f;
-                    }
-            }
-            // x fragments: instruction i takes the inputs that the weights' words hold
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int k = WT && PER == 4 ? k0 + 128 * (i / 4) + 32 * c + 8 * (i % 4) : k0 + 32 * i + 8 * c;
-                    const bool in = k < K && 16 * m + col < nr;
-                    xv[m][i] = in ? *reinterpret_cast<const uint4*>(xp[m] + k) : make_uint4(0, 0, 0, 0);
+                for (int t = 0; t < NT; ++t) {
+                    if (CUT) wv[t][i] = make_uint4(0, 0, 0, 0);
+                    if (!CUT || k < K) wv[t][i] = *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2));
                 }
-            if constexpr (WT) {
-                const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
-                const uint4 ones = make_uint4(one, one, one, one);
+            }
+            // x fragments: instruction i takes the inputs that the weights'
+            // words hold; lanes of rows past the batch load nothing
+            auto load_x = [&](int i0) {
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+#pragma unroll
+                    for (int j = 0; j < XI; ++j) xv[m][j] = make_uint4(0, 0, 0, 0);
+                    if (16 * m + col < nr) {
+#pragma unroll
+                        for (int j = 0; j < XI; ++j) {
+                            const int i = i0 + j;
+                            const int k = WT && PER == 4 ? k0 + 128 * (i / 4) + 32 * c + 8 * (i % 4) : k0 + 32 * i + 8 * c;
+                            if (!CUT || k < K) xv[m][j] = *reinterpret_cast<const uint4*>(xp[m] + k);
+                        }
+                    }
+                }
+            };
+            load_x(0);
+            if constexpr (WT && PER < 4) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (PER < 4) wv[t][i] = transpose_quarters(wv[t][i]);
+                    for (int i = 0; i < LD; ++i) wv[t][i] = transpose_quarters(wv[t][i]);
+            }
 #pragma unroll
-                for (int m = 0; m < MB; ++m)
+            for (int i0 = 0; i0 < 8; i0 += XI) {
+                if (i0) load_x(i0);
+                if constexpr (WT) {
+                    const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
+                    const uint4 ones = make_uint4(one, one, one, one);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) xv[m][i] = codes_order(xv[m][i]);
+                    for (int m = 0; m < MB; ++m)
 #pragma unroll
-                for (int g = 0; g < SG; ++g) {
-                    f32x4 acc[NT][MB] = {}, sx[MB] = {};
+                        for (int j = 0; j < XI; ++j) xv[m][j] = codes_order(xv[m][j]);
 #pragma unroll
-                    for (int p = 0; p < PER; ++p) {
-                        const int i = g * PER + p;
+                    for (int g = i0 / PER; g < (i0 + XI) / PER; ++g) {
+                        f32x4 acc[NT][MB] = {}, sx[MB] = {};
 #pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            const uint4 v = wv[t][i / 4];
-                            const uint4 f = codes_frag<DT>(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+                        for (int p = 0; p < PER; ++p) {
+                            const int i = g * PER + p;
 #pragma unroll
-                            for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xv[m][i], f, acc[t][m]);
+                            for (int t = 0; t < NT; ++t) {
+                                const uint4 v = wv[t][i / 4];
+                                const uint4 f = codes_frag<DT>(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+#pragma unroll
+                                for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xv[m][i - i0], f, acc[t][m]);
+                            }
+#pragma unroll
+                            for (int m = 0; m < MB; ++m) sx[m] = mfma16<DT>(xv[m][i - i0], ones, sx[m]);
                         }
 #pragma unroll
-                        for (int m = 0; m < MB; ++m) sx[m] = mfma16<DT>(xv[m][i], ones, sx[m]);
+                        for (int t = 0; t < NT; ++t) {
+                            const uint32_t h = s16[t][g / 2] >> (16 * (g & 1)) & 0xFFFFu;
+                            float sc = a.scale_f32 ? __uint_as_float(s32[t][g])
+                                       : DT == MOE_BF16 ? __uint_as_float(h << 16)
+                                                        : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+                            if (CUT && k0 + 32 * PER * g >= K) sc = 0.0f;
+                            const float z = a.zeros ? (float)((uint32_t)(zraw[t] >> (8 * g)) & 0xFFu) : 8.0f;
+#pragma unroll
+                            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    tot[t][m][e] = fmaf(sc, fmaf(-z, sx[m][e], acc[t][m][e]), tot[t][m][e]);
+                        }
+                        if (MB == 4) __builtin_amdgcn_sched_barrier(0);  // a group at a time: hoisted fragments spill
                     }
+                } else {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                    for (int j = 0; j < XI; ++j)
 #pragma unroll
-                        for (int m = 0; m < MB; ++m)
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                tot[t][m][e] = fmaf(sc[t][g], fmaf(-zr[t][g], sx[m][e], acc[t][m][e]), tot[t][m][e]);
+                            for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][j], wv[t][i0 + j], tot[t][m]);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][i], wv[t][i], tot[t][m]);
             }
-        }
+        };
+        int k0 = wave * kSegment;
+        for (; k0 + kSegment <= K; k0 += waves * kSegment) segment(k0, std::false_type{});
+        if (k0 < K) segment(k0, std::true_type{});
         // join the waves' parts in wave order; element (row, col) of a block
         // sits at lane 16 (row / 4) + col, component row % 4
 #pragma unroll
@@ -253,8 +322,8 @@ template <int WT, int DT, int NT, int PER, bool SWI>
 static hipError_t stream_launch_rows(const StreamArgs& a, int mb, dim3 grid, int waves, hipStream_t s) {
     const size_t lds = (size_t)waves * NT * mb * 1024;
     if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else if (mb == 2) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else if (mb == 2 || PER == 1) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else if constexpr (PER > 1) expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
 }
 
@@ -264,8 +333,8 @@ static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     const int slots = a.rows.offsets ? (a.rows.R < a.rows.S ? a.rows.R : a.rows.S) : 1;
     const int mean = (a.rows.R + slots - 1) / slots;
     // Rows a pass: twice the mean and more, so that a slot above it still
-    // takes one pass over its weights.
-    const int mb = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
+    // takes one pass over its weights; 64 rows of groups of 32 would spill.
+    const int mb = mean <= 8 ? 1 : mean <= 16 || PER == 1 ? 2 : 4;
     const int segs = (a.K + kSegment - 1) / kSegment, turns = (segs + kStreamWaves - 1) / kStreamWaves;
     const int waves = (segs + turns - 1) / turns;
     const int width = act ? a.N / 2 : a.N;

@@ -55,7 +55,7 @@ def _w4(**kw):
 
 
 @pytest.mark.parametrize("kw,want,needle", PRODUCT + [
-    (dict(group=48), UNS, "group"), (dict(group=0), UNS, "group"), (dict(group=128, K=192), UNS, "multiple of the group"),
+    (dict(group=48), UNS, "group"), (dict(group=256, K=512), UNS, "group"), (dict(group=0), UNS, "group"), (dict(group=128, K=192), UNS, "multiple of the group"),
     (dict(st=Q.MOE_F16), UNS, "scale"), (dict(q=None), INV, "NULL"), (dict(sc=None), INV, "NULL"),
     (dict(q=FAKE + 2), INV, "aligned"),
 ])
