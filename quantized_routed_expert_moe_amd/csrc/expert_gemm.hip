@@ -1,96 +1,80 @@
-// Matrix products grouped by expert over ragged batches, and the weight
-// gradient: the simple form, one output element per thread.
+// Matrix products grouped by expert over ragged batches and the weight
+// gradient: which kernel takes a call.
+#include <algorithm>
+
 #include "expert_stream.h"
+#include "expert_tile.h"
 
 namespace qmoe {
 
-// Slot that owns position q, or -1.
-__device__ __forceinline__ int slot_of_position(const RowMap& m, int q) {
-    if (!m.offsets) return 0;
-    int lo = 0, hi = m.S;  // the last slot with offsets[slot] <= q
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (m.offsets[mid] <= q) lo = mid;
-        else hi = mid;
-    }
-    const int2 r = slot_range(m, lo);
-    return q >= r.x && q < r.x + r.y ? lo : -1;
-}
-
-template <int DT, int YT>
-__global__ __launch_bounds__(256) void expert_gemm_simple(const ExpertGemmArgs a) {
-    typedef typename DType<DT>::type E;
-    const int q = blockIdx.y + gridDim.y * blockIdx.z;
-    if (q >= a.rows.R) return;
-    const int s = slot_of_position(a.rows, q);
-    if (s < 0) return;
-    const int in = a.transpose ? a.N : a.K;
-    const int out = a.transpose ? a.K : a.act ? a.N / 2 : a.N;
-    const E* x = static_cast<const E*>(a.x) + (size_t)row_of(a.rows, a.x_rows, q) * in;
-    const E* w = reinterpret_cast<const E*>(static_cast<const uint8_t*>(a.w) + (size_t)s * a.w_stride);
-    typename DType<YT>::type* y =
-        static_cast<typename DType<YT>::type*>(a.y) + (size_t)row_of(a.rows, a.y_rows, q) * out;
-    for (int c = blockIdx.x * 256 + threadIdx.x; c < out; c += gridDim.x * 256) {
-        float v = 0.f, u = 0.f;
-        if (a.transpose) {
-            for (int n = 0; n < a.N; ++n) v = fmaf((float)x[n], (float)w[(size_t)n * a.K + c], v);
-        } else {
-            for (int j = 0; j < a.K; ++j) {
-                v = fmaf((float)x[j], (float)w[(size_t)c * a.K + j], v);
-                if (a.act) u = fmaf((float)x[j], (float)w[(size_t)(c + out) * a.K + j], u);
-            }
-            if (a.act) v = v * sigmoid_f32(v) * u;
-        }
-        y[c] = (typename DType<YT>::type)v;
-    }
-}
-
-template <int DT, int YT>
-__global__ __launch_bounds__(256) void expert_wgrad_simple(const ExpertWgradArgs a) {
-    typedef typename DType<DT>::type E;
-    const int s = blockIdx.z;
-    const int2 r = slot_range(a.rows, s);
-    const int j = blockIdx.x * 256 + threadIdx.x, n = blockIdx.y;
-    if (j >= a.K) return;
-    float v = 0.f;
-    for (int q = r.x; q < r.x + r.y; ++q)
-        v = fmaf((float)static_cast<const E*>(a.dy)[(size_t)row_of(a.rows, a.dy_rows, q) * a.N + n],
-                 (float)static_cast<const E*>(a.x)[(size_t)row_of(a.rows, a.x_rows, q) * a.K + j], v);
-    static_cast<typename DType<YT>::type*>(a.dw)[((size_t)s * a.N + n) * a.K + j] = (typename DType<YT>::type)v;
-}
+// Slots that can own a position.
+static int possible_slots(const RowMap& m) { return !m.offsets ? 1 : m.S < m.R ? m.S : m.R; }
 
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
-    const int slots = a.rows.offsets && a.rows.S < a.rows.R ? a.rows.S : a.rows.offsets ? a.rows.R : 1;
-    if (!a.transpose && a.rows.R <= 32 * slots) {
+    const int slots = possible_slots(a.rows);
+    // Few rows a slot: the weights' stream bounds the call.
+    if (!a.transpose && a.rows.R <= 32ll * slots) {
         const StreamArgs t{a.x, a.w, a.w_stride, nullptr, nullptr, 0, 0, a.N, a.K, a.rows, a.x_rows, a.y_rows, a.y,
                            a.y_dtype == MOE_F32};
         return a.dtype == MOE_BF16 ? launch_stream_bf16(t, 0, a.act, s) : launch_stream_f16(t, 0, a.act, s);
     }
-    const int out = a.transpose ? a.K : a.act ? a.N / 2 : a.N;
-    const int gy = a.rows.R < 32768 ? a.rows.R : 32768;
-    const dim3 grid((out + 255) / 256, gy, (a.rows.R + gy - 1) / gy);
-    if (a.dtype == MOE_BF16) {
-        if (a.y_dtype == MOE_F32) expert_gemm_simple<MOE_BF16, MOE_F32><<<grid, 256, 0, s>>>(a);
-        else expert_gemm_simple<MOE_BF16, MOE_BF16><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (a.y_dtype == MOE_F32) expert_gemm_simple<MOE_F16, MOE_F32><<<grid, 256, 0, s>>>(a);
-        else expert_gemm_simple<MOE_F16, MOE_F16><<<grid, 256, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    TileArgs t{};
+    t.q = a.x; t.p = a.w; t.p_stride = a.w_stride; t.N = a.N; t.K = a.K; t.rows = a.rows; t.q_rows = a.x_rows;
+    t.y_rows = a.y_rows; t.y = a.y; t.y_f32 = a.y_dtype == MOE_F32; t.splits = 1;
+    // 256 x 256 tiles once they fill the 256 CUs, else 128 x 128.
+    const long long cols = a.transpose ? a.K : a.N;
+    const int big = (a.rows.R / 256 + slots) * ((cols + 255) / 256) >= 256;
+    const int mode = a.transpose ? kDataGrad : kForward;
+    return a.dtype == MOE_BF16 ? launch_tile_bf16(t, mode, a.act, big, s) : launch_tile_f16(t, mode, a.act, big, s);
 }
 
-size_t expert_wgrad_workspace_bytes(int, int, int, int) { return 0; }
+// Parts that a slot's rows are split into where the output has too few tiles
+// for the CUs: 128 x 128 tiles and parts of 512 rows and more, up to 16.
+static int wgrad_splits(int S, int N, int K, int R) {
+    const long long tiles = (long long)S * ((N + 127) / 128) * ((K + 127) / 128);
+    const long long most = std::min<long long>(16, R / S / 512);
+    return (int)std::max<long long>(1, std::min<long long>(most, 512 / tiles));
+}
+
+size_t expert_wgrad_workspace_bytes(int S, int N, int K, int R) {
+    const int splits = wgrad_splits(S, N, K, R);
+    return splits > 1 ? (size_t)splits * S * N * K * sizeof(float) : 0;
+}
+
+// dw = the sum of the parts, in part order.
+template <int DT>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ parts, int splits, size_t n, void* dw) {
+    const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= n) return;
+    float v[8];
+    load_vec8<MOE_F32>(parts, i, v);
+    for (int p = 1; p < splits; ++p) {
+        float u[8];
+        load_vec8<MOE_F32>(parts, (size_t)p * n + i, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += u[e];
+    }
+    store_vec8<DT>(dw, i, v);
+}
 
 hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
-    const dim3 grid((a.K + 255) / 256, a.N, a.rows.S);
-    if (a.dtype == MOE_BF16) {
-        if (a.dw_dtype == MOE_F32) expert_wgrad_simple<MOE_BF16, MOE_F32><<<grid, 256, 0, s>>>(a);
-        else expert_wgrad_simple<MOE_BF16, MOE_BF16><<<grid, 256, 0, s>>>(a);
-    } else {
-        if (a.dw_dtype == MOE_F32) expert_wgrad_simple<MOE_F16, MOE_F32><<<grid, 256, 0, s>>>(a);
-        else expert_wgrad_simple<MOE_F16, MOE_F16><<<grid, 256, 0, s>>>(a);
-    }
+    TileArgs t{};
+    t.q = a.dy; t.p = a.x; t.N = a.N; t.K = a.K; t.rows = a.rows; t.q_rows = a.dy_rows; t.p_rows = a.x_rows;
+    t.splits = wgrad_splits(a.rows.S, a.N, a.K, a.rows.R);
+    t.y = t.splits > 1 ? a.ws : a.dw;
+    t.y_f32 = t.splits > 1 || a.dw_dtype == MOE_F32;
+    const long long tiles = (long long)a.rows.S * ((a.N + 255) / 256) * ((a.K + 255) / 256);
+    const int big = t.splits == 1 && tiles >= 256;
+    const hipError_t e = a.dtype == MOE_BF16 ? launch_tile_bf16(t, kWeightGrad, 0, big, s)
+                                             : launch_tile_f16(t, kWeightGrad, 0, big, s);
+    if (e != hipSuccess || t.splits == 1) return e;
+    const size_t n = (size_t)a.rows.S * a.N * a.K;
+    const dim3 grid((uint32_t)((n / 8 + 255) / 256));
+    const float* parts = static_cast<const float*>(a.ws);
+    if (a.dw_dtype == MOE_F32) wgrad_join_kernel<MOE_F32><<<grid, 256, 0, s>>>(parts, t.splits, n, a.dw);
+    else if (a.dw_dtype == MOE_BF16) wgrad_join_kernel<MOE_BF16><<<grid, 256, 0, s>>>(parts, t.splits, n, a.dw);
+    else wgrad_join_kernel<MOE_F16><<<grid, 256, 0, s>>>(parts, t.splits, n, a.dw);
     return hipGetLastError();
 }
 
