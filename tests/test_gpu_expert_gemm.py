@@ -69,6 +69,26 @@ def test_product_swiglu(sizes, N, K, dtype, out):
     run_product(sizes, N, K, dtype, out, act=Q.MOE_ACT_SWIGLU, seed=N)
 
 
+LARGE = [300, 0, 257, 1, 64, 65, 33, 128, 129, 200, 255, 256, 31, 32, 320, 97] * 2  # every count of 32-row blocks
+
+
+@pytest.mark.parametrize("inner", [8, 64, 72, 128, 136, 192, 200, 256, 264, 328, 392, 584])
+@pytest.mark.parametrize("transpose", [False, True])
+def test_product_large_tiles(inner, transpose):
+    """Enough tiles for the 256 x 256 kernels, every count of contraction stages and rests."""
+    N, K = (inner, 2824) if transpose else (2824, inner)
+    run_product(LARGE, N, K, BF, BF, transpose=transpose, seed=inner)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, F32), (HF, HF), (HF, F32)])
+@pytest.mark.parametrize("mode", ["forward", "transpose", "swiglu"])
+def test_product_large_tiles_types(dtype, out, mode):
+    N, K = (328, 2824) if mode == "transpose" else (2832, 328)
+    k, P = 2, sum(LARGE) + 100
+    run_product(LARGE, N, K, dtype, out, k=k, P=P, x_rows=PAIR if mode == "transpose" else TOKEN,
+                y_rows=POS if mode == "swiglu" else PAIR, transpose=mode == "transpose", act=int(mode == "swiglu"), seed=3)
+
+
 def test_product_larger_weight_stride():
     run_product([3, 40], 72, 80, BF, BF, pad=64, seed=5)
     run_product([200, 140], 72, 80, BF, BF, pad=64, seed=6)
@@ -149,6 +169,14 @@ def test_weight_gradient_of_ragged_slots(sizes, dtype, out):
 @pytest.mark.parametrize("rows", [1, 70, 2049])
 def test_weight_gradient_odd_sizes(N, K, rows):
     run_wgrad([rows, 0, rows // 3 + 1], N, K, BF, F32, seed=rows)
+
+
+@pytest.mark.parametrize("dtype,out", [(BF, F32), (HF, HF)])
+@pytest.mark.parametrize("dy_rows,x_rows", [(POS, POS), (PAIR, TOKEN)])
+def test_weight_gradient_large_tiles(dtype, out, dy_rows, x_rows):
+    """Enough tiles for the 256 x 256 kernels, every count of row stages, slots beyond the window of source rows."""
+    sizes = [0, 1, 63, 64, 65, 128, 129, 192, 193, 256, 257, 320, 321, 1100, 2500, 1024, 1025]
+    run_wgrad(sizes, 1032, 1048, dtype, out, k=2, P=sum(sizes) + 64, dy_rows=dy_rows, x_rows=x_rows, seed=2)
 
 
 @pytest.mark.parametrize("dy_rows", [POS, PAIR, TOKEN])
