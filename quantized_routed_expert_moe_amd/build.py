@@ -21,7 +21,8 @@ HOST_SO = os.path.join(HERE, "libqmoe_host.so")  # host leg + residency policy (
 SOURCES = ["abi.cpp", "route.hip", "batches.hip", "route_batches.hip", "ffn_decode.hip", "ffn_prefill.hip",
            "combine.hip", "layer_decode.hip", "hbm_probe.hip", "prefill_probe.hip", "ffn_prefill_i8.hip",
            "abi_ops.cpp", "expert_gemm.hip", "expert_w4.hip", "expert_stream_bf16.hip",
-           "expert_stream_f16.hip", "expert_tile_bf16.hip", "expert_tile_f16.hip", "block_norm.hip", "swiglu.hip"]
+           "expert_stream_f16.hip", "expert_tile_bf16.hip", "expert_tile_f16.hip", "block_norm.hip", "block_norm_f32.hip",
+           "block_norm_bf16.hip", "block_norm_f16.hip", "swiglu.hip"]
 # ffn_prefill.hip is compiled once more per block type with only that type's
 # GEMM kernels (QMOE_PREFILL_FMT), so the types compile in parallel.
 PREFILL_TYPES = [1, 2, 3, 4, 5]
