@@ -439,13 +439,16 @@ MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 
 _torch = None
+_raw_stream = None  # device -> its current stream's handle, without building a Stream object
 _CODES = {}  # torch dtype -> moe_dtype
 _I32 = _U8 = None
 
 
 def _op_types() -> None:
-    global _torch, _I32, _U8
+    global _torch, _raw_stream, _I32, _U8
     import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
     _CODES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
     _I32, _U8 = torch.int32, torch.uint8
     _torch = torch
@@ -479,9 +482,9 @@ def _op_device() -> int:
     return _torch.cuda.current_device()
 
 
-def _op_stream(stream) -> int:
+def _op_stream(device: int, stream) -> int:
     if stream is None:
-        stream = _torch.cuda.current_stream()
+        return _raw_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -520,7 +523,7 @@ def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: i
     xp, wp, op, pp, yp = _op_ptrs(dev, x=x, w=w[0], slot_offsets=slot_offsets, perm_pair=perm_pair, y=y)
     _check(lib().moe_expert_gemm(xp, _op_code(x, "x"), wp, 2 * (w.stride(0) if S > 1 else N * K), S, N, K,
                                  int(bool(transpose)), op, R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"),
-                                 _op_stream(stream)))
+                                 _op_stream(dev, stream)))
 
 
 def moe_expert_gemm_wgrad_workspace_size(S: int, N: int, K: int, R: int) -> int:
@@ -542,7 +545,7 @@ def moe_expert_gemm_wgrad(dy, x, slot_offsets, dw, perm_pair=None, k: int = 1, d
     dp, xp, op, pp, wp, sp = _op_ptrs(dev, dy=dy, x=x, slot_offsets=slot_offsets, perm_pair=perm_pair, dw=dw, ws=ws)
     _check(lib().moe_expert_gemm_wgrad(dp, xp, _op_code(x, "x"), S, N, K, op, R, pp, k, dy_rows, x_rows, wp,
                                        _op_code(dw, "dw"), sp, 0 if ws is None else ws.numel() * ws.element_size(),
-                                       _op_stream(stream)))
+                                       _op_stream(dev, stream)))
 
 
 def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pair=None, k: int = 1,
@@ -563,7 +566,7 @@ def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pa
     xp, qp, sp, zp, op, pp, yp = _op_ptrs(dev, x=x, q=q, scales=scales, zeros=zeros, slot_offsets=slot_offsets,
                                           perm_pair=perm_pair, y=y)
     _check(lib().moe_expert_gemv_w4(xp, _op_code(x, "x"), qp, sp, _op_code(scales, "scales"), zp, group, S, N, K, op,
-                                    R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"), _op_stream(stream)))
+                                    R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"), _op_stream(dev, stream)))
 
 
 def _norm_shapes(x, y, w_post, gate, w_pre) -> tuple:
@@ -607,7 +610,7 @@ def moe_block_norm(x, y, w_post, gate, w_pre, x_out, h, eps: float, res_scale: f
     _norm_like(h, x, "h")
     xp, yp, wp, gp, np_, op, hp = _op_ptrs(dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, x_out=x_out, h=h)
     _check(lib().moe_block_norm(xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_,
-                                w_code, T, H, eps, res_scale, op, hp, _op_stream(stream)))
+                                w_code, T, H, eps, res_scale, op, hp, _op_stream(dev, stream)))
 
 
 def moe_block_norm_backward_workspace_size(T: int, H: int) -> int:
@@ -633,7 +636,7 @@ def moe_block_norm_backward(x, y, w_post, gate, w_pre, dx_out, dh, dx, dy, dw_po
     _check(lib().moe_block_norm_backward(
         xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_, w_code, T, H, eps,
         res_scale, op, hp, dxp, dyp, d0, d1, d2, sp, 0 if ws is None else ws.numel() * ws.element_size(),
-        _op_stream(stream)))
+        _op_stream(dev, stream)))
 
 
 def _swiglu_shapes(gu, slot_offsets, **halves) -> tuple:
@@ -656,7 +659,7 @@ def moe_swiglu(gu, h, slot_offsets=None, stream=None):
     dev = _op_device()
     R, I, S = _swiglu_shapes(gu, slot_offsets, h=h)
     gp, op, hp = _op_ptrs(dev, gu=gu, slot_offsets=slot_offsets, h=h)
-    _check(lib().moe_swiglu(gp, _op_code(gu, "gu"), R, I, op, S, hp, _op_stream(stream)))
+    _check(lib().moe_swiglu(gp, _op_code(gu, "gu"), R, I, op, S, hp, _op_stream(dev, stream)))
 
 
 def moe_swiglu_backward(gu, dh, dgu, h=None, slot_offsets=None, stream=None):
@@ -665,7 +668,7 @@ def moe_swiglu_backward(gu, dh, dgu, h=None, slot_offsets=None, stream=None):
     R, I, S = _swiglu_shapes(gu, slot_offsets, dh=dh, h=h)
     _norm_like(dgu, gu, "dgu")
     gp, dp, op, up, hp = _op_ptrs(dev, gu=gu, dh=dh, slot_offsets=slot_offsets, dgu=dgu, h=h)
-    _check(lib().moe_swiglu_backward(gp, dp, _op_code(gu, "gu"), R, I, op, S, up, hp, _op_stream(stream)))
+    _check(lib().moe_swiglu_backward(gp, dp, _op_code(gu, "gu"), R, I, op, S, up, hp, _op_stream(dev, stream)))
 
 
 # ------------------------------------------------------------ host leg

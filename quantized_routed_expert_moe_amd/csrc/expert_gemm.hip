@@ -13,8 +13,11 @@ static int possible_slots(const RowMap& m) { return !m.offsets ? 1 : m.S < m.R ?
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
     const int slots = possible_slots(a.rows);
-    // Few rows a slot: the weights' stream bounds the call.
-    if (!a.transpose && a.rows.R <= 32ll * slots) {
+    // Few rows a slot: the weights' stream bounds the call.  64 experts of 4096 x
+    // 2048 take 225 us streamed and 259 us tiled at 16 rows each, 313 and 266
+    // us at 48; one matrix of 2048 x 2048 takes 12.6 and 19.3 us at 64 rows, 23.1
+    // and 22.0 us at 128.
+    if (!a.transpose && (a.rows.R <= 24ll * slots || a.rows.R <= 64)) {
         const StreamArgs t{a.x, a.w, a.w_stride, nullptr, nullptr, 0, 0, a.N, a.K, a.rows, a.x_rows, a.y_rows, a.y,
                            a.y_dtype == MOE_F32};
         return a.dtype == MOE_BF16 ? launch_stream_bf16(t, 0, a.act, s) : launch_stream_f16(t, 0, a.act, s);

@@ -177,6 +177,15 @@ __device__ __forceinline__ int row_of(const RowMap& m, int how, int q) {
     return how == MOE_ROWS_PAIR ? p : p / m.k;
 }
 
+// row_of in two parts: the pair (or position) as loaded, and its row.
+__device__ __forceinline__ int pair_of(const RowMap& m, int how, int q) {
+    return how == MOE_ROWS_POSITION ? q : m.perm[q];
+}
+__device__ __forceinline__ int row_of_pair(const RowMap& m, int how, int p) {
+    p = min(max(p, 0), m.R - 1);
+    return how == MOE_ROWS_TOKEN ? p / m.k : p;
+}
+
 #endif  // __HIPCC__
 
 }  // namespace qmoe

@@ -47,7 +47,10 @@ struct StreamArgs {
 };
 
 constexpr int kSegment = 256;  // inputs a wave takes at a time
-constexpr int kStreamWaves = 8;
+// Waves that split a workgroup's inputs.  Four: more would leave a CU one or
+// two workgroups (128 experts of 4096 x 7168 at 12 rows a slot takes 671
+// us, with eight 792 us).
+constexpr int kStreamWaves = 4;
 
 template <int DT>
 __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
@@ -91,6 +94,20 @@ __device__ __forceinline__ uint4 transpose_quarters(uint4 v) {
     const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
     const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
     return make_uint4(c[0], c[1], d[0], d[1]);
+}
+
+// An unaligned load.
+template <typename T>
+__device__ __forceinline__ T load_bytes(const uint8_t* p) {
+    T v;
+    __builtin_memcpy(&v, p, sizeof v);
+    return v;
+}
+
+// The value that the first quarter's lane of the same lane % 16 holds.
+__device__ __forceinline__ uint32_t first_quarter(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
 }
 
 // Slot of index i: with fewer positions than slots the i-th slot that owns
@@ -144,100 +161,125 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
     }
     for (int rb = 0; rb < r.y; rb += 16 * MB) {
         const int nr = min(r.y - rb, 16 * MB);
-        const E* xp[MB];
+        // The lane's x rows: requested first, turned into addresses only behind
+        // the first weight loads, so that those do not wait for them.
+        int xrow[MB];
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const int i = min(16 * m + col, nr - 1);
-            xp[m] = static_cast<const E*>(a.x) + (size_t)row_of(a.rows, a.x_rows, r.x + rb + i) * K;
-        }
+        for (int m = 0; m < MB; ++m) xrow[m] = pair_of(a.rows, a.x_rows, r.x + rb + min(16 * m + col, nr - 1));
         f32x4 tot[NT][MB] = {};
-        // One segment of 256 inputs.  Every load is issued before the first
-        // use; only the last segment of a row may be cut, and only its copy of
-        // the code tests inputs (one body for both would merge their registers
-        // at the price of a wait behind each load).
-        auto segment = [&](int k0, auto cut_tag) {
-            constexpr bool CUT = decltype(cut_tag)::value;
-            constexpr int LD = WT ? 2 : 8;          // 16-byte weight loads a tile
-            constexpr int SG = WT ? 8 / PER : 2;    // groups of the segment
-            constexpr int XI = MB == 4 ? 4 : 8;     // x instructions held at a time: 64 rows of eight would spill
-            typedef uint32_t s16v __attribute__((ext_vector_type(SG / 2)));
-            typedef uint32_t s32v __attribute__((ext_vector_type(SG)));
-            uint4 wv[NT][LD], xv[MB][XI];
-            s16v s16[NT];
-            s32v s32[NT];
-            uint64_t zraw[NT];
-            if constexpr (WT) {
-                // A row's groups of the segment lie side by side: one load of up
-                // to 16 bytes (2- or 1-byte aligned), since single values cost
-                // the address unit a lane at a time.  They come first: the branch
-                // on their type costs a wait for what is in flight.
-                auto at = [&](int t, int g) { return sp[t] + (min(k0 + 32 * PER * g, K - 1) >> a.group_shift); };
-                if (a.scale_f32) {
+        // A segment of 256 inputs: its weights, scales and zeros as loaded.
+        constexpr int LD = WT ? 2 : 8;        // 16-byte weight loads a tile
+        constexpr int SG = WT ? 8 / PER : 2;  // groups of the segment
+        constexpr int XI = MB == 4 ? 4 : 8;   // x instructions held at a time: 64 rows of eight would spill
+        typedef uint32_t s16v __attribute__((ext_vector_type(SG / 2)));
+        typedef uint32_t s32v __attribute__((ext_vector_type(SG)));
+        auto run = [&](auto scale_tag, auto zero_tag) {
+            constexpr bool SCALE_F32 = decltype(scale_tag)::value, ZEROS = decltype(zero_tag)::value;
+            struct Segment {
+                uint4 w[NT][LD];
+                s16v s16[NT];
+                s32v s32[NT];
+                uint64_t z[NT];
+            };
+            // CUT: the row's last segment, shorter than 256
+            auto load = [&](Segment& v, int k0, auto cut_tag) {
+                constexpr bool CUT = decltype(cut_tag)::value;
+#pragma unroll
+                for (int i = 0; i < LD; ++i) {
+                    const int k = WT ? k0 + 128 * i + 32 * c : k0 + 32 * i + 8 * c;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const uint32_t* p = static_cast<const uint32_t*>(a.scales);
-                        if (!CUT) __builtin_memcpy(&s32[t], p + at(t, 0), 4 * SG);
-                        else
-#pragma unroll
-                            for (int g = 0; g < SG; ++g) s32[t][g] = p[at(t, g)];
+                        if (CUT) v.w[t][i] = make_uint4(0, 0, 0, 0);
+                        if (!CUT || k < K) v.w[t][i] = *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2));
                     }
-                } else {
+                }
+                if constexpr (WT) {
+                    // A row's groups of the segment lie side by side: one load of
+                    // up to 16 bytes (2- or 1-byte aligned), since single values
+                    // cost the address unit a lane at a time.
+                    // The four quarters want the same values: the first loads them.
+                    auto at = [&](int t, int g) { return sp[t] + (min(k0 + 32 * PER * g, K - 1) >> a.group_shift); };
+                    if (CUT || c == 0)
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const uint16_t* p = static_cast<const uint16_t*>(a.scales);
-                        if (!CUT) __builtin_memcpy(&s16[t], p + at(t, 0), 2 * SG);
-                        else
+                        if constexpr (SCALE_F32) {
+                            const uint32_t* p = static_cast<const uint32_t*>(a.scales);
+                            if (!CUT) __builtin_memcpy(&v.s32[t], p + at(t, 0), 4 * SG);
+                            else
 #pragma unroll
-                            for (int g = 0; g < SG; g += 2) s16[t][g / 2] = p[at(t, g)] | (uint32_t)p[at(t, g + 1)] << 16;
+                                for (int g = 0; g < SG; ++g) v.s32[t][g] = p[at(t, g)];
+                        } else {
+                            const uint16_t* p = static_cast<const uint16_t*>(a.scales);
+                            if (!CUT) __builtin_memcpy(&v.s16[t], p + at(t, 0), 2 * SG);
+                            else
+#pragma unroll
+                                for (int g = 0; g < SG; g += 2) v.s16[t][g / 2] = p[at(t, g)] | (uint32_t)p[at(t, g + 1)] << 16;
+                        }
+                        if constexpr (ZEROS) {
+                            v.z[t] = 0;
+                            if (!CUT) {
+                                if constexpr (SG == 2) v.z[t] = load_bytes<uint16_t>(a.zeros + at(t, 0));
+                                else if constexpr (SG == 4) v.z[t] = load_bytes<uint32_t>(a.zeros + at(t, 0));
+                                else v.z[t] = load_bytes<uint64_t>(a.zeros + at(t, 0));
+                            } else
+#pragma unroll
+                                for (int g = 0; g < SG; ++g) v.z[t] |= (uint64_t)a.zeros[at(t, g)] << (8 * g);
+                        }
                     }
                 }
-                if (a.zeros) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        zraw[t] = 0;
-                        if (!CUT) __builtin_memcpy(&zraw[t], a.zeros + at(t, 0), SG);
-                        else
-#pragma unroll
-                            for (int g = 0; g < SG; ++g) zraw[t] |= (uint64_t)a.zeros[at(t, g)] << (8 * g);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < LD; ++i) {
-                const int k = WT ? k0 + 128 * i + 32 * c : k0 + 32 * i + 8 * c;
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (CUT) wv[t][i] = make_uint4(0, 0, 0, 0);
-                    if (!CUT || k < K) wv[t][i] = *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2));
-                }
-            }
+            };
+            uint4 xv[MB][XI];
             // x fragments: instruction i takes the inputs that the weights'
             // words hold; lanes of rows past the batch load nothing
-            auto load_x = [&](int i0) {
+            auto load_x = [&](int k0, int i0, auto cut_tag) {
+                constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
+                    if (CUT)
 #pragma unroll
-                    for (int j = 0; j < XI; ++j) xv[m][j] = make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < XI; ++j) xv[m][j] = make_uint4(0, 0, 0, 0);
+                    int row = xrow[m];
+                    asm("" : "+v"(row));  // not hoisted above the weight loads
+                    const E* xp = static_cast<const E*>(a.x) + (size_t)row_of_pair(a.rows, a.x_rows, row) * K;
                     if (16 * m + col < nr) {
 #pragma unroll
                         for (int j = 0; j < XI; ++j) {
                             const int i = i0 + j;
                             const int k = WT && PER == 4 ? k0 + 128 * (i / 4) + 32 * c + 8 * (i % 4) : k0 + 32 * i + 8 * c;
-                            if (!CUT || k < K) xv[m][j] = *reinterpret_cast<const uint4*>(xp[m] + k);
+                            if (!CUT || k < K) xv[m][j] = *reinterpret_cast<const uint4*>(xp + k);
                         }
                     }
                 }
             };
-            load_x(0);
-            if constexpr (WT && PER < 4) {
+            // what stands between a segment's loads and its use
+            auto arrange = [&](Segment& v, auto cut_tag) {
+                if constexpr (WT && !decltype(cut_tag)::value) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                    for (int t = 0; t < NT; ++t) {
+                        if constexpr (SCALE_F32) {
 #pragma unroll
-                    for (int i = 0; i < LD; ++i) wv[t][i] = transpose_quarters(wv[t][i]);
-            }
+                            for (int g = 0; g < SG; ++g) v.s32[t][g] = first_quarter(v.s32[t][g]);
+                        } else {
 #pragma unroll
-            for (int i0 = 0; i0 < 8; i0 += XI) {
-                if (i0) load_x(i0);
+                            for (int g = 0; g < SG / 2; ++g) v.s16[t][g] = first_quarter(v.s16[t][g]);
+                        }
+                        if constexpr (ZEROS) {
+                            const uint32_t lo = first_quarter((uint32_t)v.z[t]);
+                            const uint32_t hi = SG > 4 ? first_quarter((uint32_t)(v.z[t] >> 32)) : 0u;
+                            v.z[t] = (uint64_t)hi << 32 | lo;
+                        }
+                    }
+                }
+                if constexpr (WT && PER < 4) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < LD; ++i) v.w[t][i] = transpose_quarters(v.w[t][i]);
+                }
+            };
+            // x instructions i0 .. i0 + XI of a segment
+            auto multiply = [&](const Segment& v, int k0, int i0, auto cut_tag) {
+                constexpr bool CUT = decltype(cut_tag)::value;
                 if constexpr (WT) {
                     const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
                     const uint4 ones = make_uint4(one, one, one, one);
@@ -253,8 +295,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
                             const int i = g * PER + p;
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const uint4 v = wv[t][i / 4];
-                                const uint4 f = codes_frag<DT>(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+                                const uint4 u = v.w[t][i / 4];
+                                const uint4 f = codes_frag<DT>(i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w);
 #pragma unroll
                                 for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xv[m][i - i0], f, acc[t][m]);
                             }
@@ -263,12 +305,16 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const uint32_t h = s16[t][g / 2] >> (16 * (g & 1)) & 0xFFFFu;
-                            float sc = a.scale_f32 ? __uint_as_float(s32[t][g])
-                                       : DT == MOE_BF16 ? __uint_as_float(h << 16)
-                                                        : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+                            float sc;
+                            if constexpr (SCALE_F32) {
+                                sc = __uint_as_float(v.s32[t][g]);
+                            } else {
+                                const uint32_t h = v.s16[t][g / 2] >> (16 * (g & 1)) & 0xFFFFu;
+                                sc = DT == MOE_BF16 ? __uint_as_float(h << 16)
+                                                    : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+                            }
                             if (CUT && k0 + 32 * PER * g >= K) sc = 0.0f;
-                            const float z = a.zeros ? (float)((uint32_t)(zraw[t] >> (8 * g)) & 0xFFu) : 8.0f;
+                            const float z = ZEROS ? (float)((uint32_t)(v.z[t] >> (8 * g)) & 0xFFu) : 8.0f;
 #pragma unroll
                             for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -283,13 +329,42 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][j], wv[t][i0 + j], tot[t][m]);
+                            for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][j], v.w[t][i0 + j], tot[t][m]);
+                }
+            };
+            const int step = waves * kSegment;
+            int k0 = wave * kSegment;
+            // (Loading the next segment while this one multiplies costs a quarter
+            // of the waves their registers and gains nothing.)
+            for (; k0 + kSegment <= K; k0 += step) {
+                Segment now;
+                load(now, k0, std::false_type{});
+                load_x(k0, 0, std::false_type{});
+                arrange(now, std::false_type{});
+#pragma unroll
+                for (int i0 = 0; i0 < 8; i0 += XI) {
+                    if (i0) load_x(k0, i0, std::false_type{});
+                    multiply(now, k0, i0, std::false_type{});
+                }
+            }
+            if (k0 < K) {
+                Segment now;
+                load(now, k0, std::true_type{});
+                load_x(k0, 0, std::true_type{});
+                arrange(now, std::true_type{});
+#pragma unroll
+                for (int i0 = 0; i0 < 8; i0 += XI) {
+                    if (i0) load_x(k0, i0, std::true_type{});
+                    multiply(now, k0, i0, std::true_type{});
                 }
             }
         };
-        int k0 = wave * kSegment;
-        for (; k0 + kSegment <= K; k0 += waves * kSegment) segment(k0, std::false_type{});
-        if (k0 < K) segment(k0, std::true_type{});
+        // one loop for each kind of scales and zeros: a branch on them between
+        // the loads costs a wait for what is in flight
+        if (WT && a.scale_f32 && a.zeros) run(std::true_type{}, std::true_type{});
+        else if (WT && a.scale_f32) run(std::true_type{}, std::false_type{});
+        else if (WT && a.zeros) run(std::false_type{}, std::true_type{});
+        else run(std::false_type{}, std::false_type{});
         // join the waves' parts in wave order; element (row, col) of a block
         // sits at lane 16 (row / 4) + col, component row % 4
 #pragma unroll
@@ -334,7 +409,7 @@ static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     const int mean = (a.rows.R + slots - 1) / slots;
     // Rows a pass: twice the mean and more, so that a slot above it still
     // takes one pass over its weights; 64 rows of groups of 32 would spill.
-    const int mb = mean <= 8 ? 1 : mean <= 16 || PER == 1 ? 2 : 4;
+    const int mb = mean <= 8 || a.rows.R <= 16 ? 1 : mean <= 16 || a.rows.R <= 32 || PER == 1 ? 2 : 4;
     const int segs = (a.K + kSegment - 1) / kSegment, turns = (segs + kStreamWaves - 1) / kStreamWaves;
     const int waves = (segs + turns - 1) / turns;
     const int width = act ? a.N / 2 : a.N;

@@ -72,6 +72,7 @@ __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // Four consecutive values in their output type, from fp32 (one rounding).
@@ -315,9 +316,11 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
     // of the count behind the loop would leave two copies of the accumulators.
     auto begin = [&](int buf) {
         load(0, buf, std::true_type{});
-        wait_loads<0>();
-        stage_barrier();
+        __builtin_amdgcn_sched_barrier(0);
         load(1, buf ^ 1, std::true_type{});
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<UQ + UP>();  // stage 0's
+        stage_barrier();
         read(0, buf, 0);
     };
     const std::integral_constant<int, kWhole> whole;
@@ -387,7 +390,14 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
             if (row >= nq || c >= width) continue;
             const size_t out = C::MODE == kWeightGrad ? ((size_t)slot * N + q0 + row) * K + c
                                                       : (size_t)row_of(a.rows, a.y_rows, q0 + row) * width + c;
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.y) + out * ES) = u;
+            uint8_t* at = static_cast<uint8_t*>(a.y) + out * ES;
+            // A weight gradient is not read again soon: past the caches it takes
+            // 316 instead of 386 us (64 experts of 1536 x 2048, fp32, 280 to 2244
+            // rows each).
+            if (C::MODE == kWeightGrad)
+                __builtin_nontemporal_store(__builtin_bit_cast(u32x4, u), reinterpret_cast<u32x4*>(at));
+            else
+                *reinterpret_cast<uint4*>(at) = u;
         }
     };
 #pragma unroll
