@@ -8,11 +8,11 @@
 // A workgroup computes a BQ x BP tile of the output; BP runs along the
 // output's contiguous dimension.  v_mfma_f32_32x32x16 takes the P operand as
 // its A matrix, so a lane ends with four consecutive output columns of one
-// row and the epilogue packs them without shuffles.  Each of the four waves
-// owns a quarter of the tile: LDS delivers 128 bytes a clock, so a 128 x 128
-// quarter (32 flops a byte read and 8 of every 12 LDS clocks of the matrix
-// instructions' time) leaves the matrix cores the limit where 128 x 64 for
-// eight waves does not.
+// row and the epilogue packs them without shuffles.  256 x 256 by eight waves of
+// 128 x 64 where such tiles fill the chip, else 128 x 128 by four of 64 x 64.
+// Measured for 8192 x 8192 x 8192 (bf16): 1290 TFLOP/s forward, 1280 data
+// gradient; four waves of 128 x 128 and rings of more, shorter stages were
+// slower, and two 256 x 128 tiles a CU as well.
 //
 // The contraction advances 64 a stage through two LDS buffers, filled by
 // global_load_lds_dwordx4 (no register staging).  A stage is four steps of 16;
@@ -86,10 +86,10 @@ __device__ __forceinline__ uint2 pack4(const float* v) {
     return __builtin_bit_cast(uint2, u);
 }
 
-// QI x PI blocks of 32 x 32 a wave, WQ x WP waves, NBUF buffers.
-template <int DT_, int MODE_, bool SWI_, int QI_, int PI_, int WQ_, int WP_, int NBUF_>
+// QI x PI blocks of 32 x 32 a wave, WQ x WP waves.
+template <int DT_, int MODE_, bool SWI_, int QI_, int PI_, int WQ_, int WP_>
 struct Tile {
-    static constexpr int DT = DT_, MODE = MODE_, QI = QI_, PI = PI_, WQ = WQ_, WP = WP_, NBUF = NBUF_;
+    static constexpr int DT = DT_, MODE = MODE_, QI = QI_, PI = PI_, WQ = WQ_, WP = WP_, NBUF = 2;
     static constexpr bool SWI = SWI_;
     static constexpr int BK = 64;
     static constexpr int W = WQ * WP, THREADS = 64 * W;
@@ -133,13 +133,14 @@ __device__ __forceinline__ void stage_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// READS LDS reads and LOADS loads to LDS spread evenly behind M matrix
-// instructions.
+// LOADS loads to LDS spread evenly behind M matrix instructions, READS LDS
+// reads behind the first half of them: their values are due next.
 template <int M, int READS, int LOADS, int I = 0>
 __device__ __forceinline__ void spread() {
     if constexpr (I < M) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        constexpr int reads = READS * (I + 1) / M - READS * I / M, loads = LOADS * (I + 1) / M - LOADS * I / M;
+        constexpr int H = (M + 1) / 2, reads = I < H ? READS * (I + 1) / H - READS * I / H : 0;
+        constexpr int loads = LOADS * (I + 1) / M - LOADS * I / M;
         if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
         if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x010, loads, 0);
         spread<M, READS, LOADS, I + 1>();
@@ -210,12 +211,20 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
     auto refill = [&](int st) {  // before the loads of stages st + 2 and st + 3
         if (MODE == kWeightGrad && filled < len && (st + 4) * BK > filled) fill_rows(C::WINDOW / 2);
     };
+    // Slots begin the contraction at different stages: at one stage all CUs
+    // would read the same 128 bytes of their rows, and rows of 2^n bytes put
+    // those into a few memory channels (128 slots of 64 rows, 1536 x 2048: 206 us
+    // in step, 159 us so; the data gradient reads whole rows, 163 and 165 us).
+    // The order of a row's sums then depends on its slot's number alone.
+    const int wholes = len / BK;
+    const int rotation = MODE == kForward && wholes > 0 ? (int)(5u * (uint32_t)slot % (uint32_t)wholes) : 0;
     // Stage st's loads.  No branch, so that they can stand between matrix
     // instructions.  REST: what lies behind the contraction's end is selected
     // away (the stage may lie behind it as a whole); else the stage is whole.
     auto load = [&](int st, int buf, auto rest) {
         constexpr bool REST = decltype(rest)::value;
         uint8_t *sq = lds.q[buf], *sp = lds.p[buf];
+        if (MODE == kForward && st < wholes) st = st + rotation < wholes ? st + rotation : st + rotation - wholes;
         uint32_t k0 = (uint32_t)st * BK;
         asm("" : "+s"(k0));  // keeps the addresses out of the loop's registers
         const int left = len - (int)k0;
@@ -465,21 +474,13 @@ template <typename C>
 __global__ __launch_bounds__(C::THREADS, C::QI * C::PI == 4 ? 2 : 1) void expert_tile_kernel(const TileArgs a) {
     // One array for each buffer, so that the compiler can tell the loads into
     // one from the reads of the others.
-#define TILE_BUFFER(i)                                                                      \
-    __shared__ __attribute__((aligned(16))) uint8_t sq##i[C::NBUF > i ? C::QBYTES : 16];    \
-    __shared__ __attribute__((aligned(16))) uint8_t sp##i[C::NBUF > i ? C::PBYTES : 16];
-    TILE_BUFFER(0) TILE_BUFFER(1) TILE_BUFFER(2) TILE_BUFFER(3)
-#undef TILE_BUFFER
+    __shared__ __attribute__((aligned(16))) uint8_t sq0[C::QBYTES], sq1[C::QBYTES], sp0[C::PBYTES], sp1[C::PBYTES];
     __shared__ int32_t srow[C::MODE == kWeightGrad ? 2 * C::WINDOW : 1];
-    static_assert(C::NBUF <= 4, "buffers");
     TileLds<C> lds;
-    uint8_t* const bq[4] = {sq0, sq1, sq2, sq3};
-    uint8_t* const bp[4] = {sp0, sp1, sp2, sp3};
-#pragma unroll
-    for (int u = 0; u < C::NBUF; ++u) {
-        lds.q[u] = bq[u];
-        lds.p[u] = bp[u];
-    }
+    lds.q[0] = sq0;
+    lds.q[1] = sq1;
+    lds.p[0] = sp0;
+    lds.p[1] = sp1;
     lds.row[0] = srow;
     lds.row[1] = srow + C::WINDOW;
 
@@ -534,18 +535,17 @@ static hipError_t tile_launch(const TileArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-#ifndef TILE_BIG
-#define TILE_BIG 4, 2, 2, 4, 2
-#endif
-#ifndef TILE_SMALL
-#define TILE_SMALL 2, 2, 2, 2, 2
-#endif
+// 256 x 256 by eight waves of 128 x 64, 128 x 128 by four of 64 x 64.
+template <int DT, int MODE, bool SWI>
+static hipError_t tile_launch_size(const TileArgs& a, int big, hipStream_t s) {
+    return big ? tile_launch<Tile<DT, MODE, SWI, 4, 2, 2, 4>>(a, s) : tile_launch<Tile<DT, MODE, SWI, 2, 2, 2, 2>>(a, s);
+}
+
 template <int DT>
 static hipError_t tile_launch_type(const TileArgs& a, int mode, int act, int big, hipStream_t s) {
-    if (mode == kForward && act) return big ? tile_launch<Tile<DT, kForward, true, TILE_BIG>>(a, s) : tile_launch<Tile<DT, kForward, true, TILE_SMALL>>(a, s);
-    if (mode == kForward) return big ? tile_launch<Tile<DT, kForward, false, TILE_BIG>>(a, s) : tile_launch<Tile<DT, kForward, false, TILE_SMALL>>(a, s);
-    if (mode == kDataGrad) return big ? tile_launch<Tile<DT, kDataGrad, false, TILE_BIG>>(a, s) : tile_launch<Tile<DT, kDataGrad, false, TILE_SMALL>>(a, s);
-    return big ? tile_launch<Tile<DT, kWeightGrad, false, TILE_BIG>>(a, s) : tile_launch<Tile<DT, kWeightGrad, false, TILE_SMALL>>(a, s);
+    if (mode == kForward) return act ? tile_launch_size<DT, kForward, true>(a, big, s) : tile_launch_size<DT, kForward, false>(a, big, s);
+    if (mode == kDataGrad) return tile_launch_size<DT, kDataGrad, false>(a, big, s);
+    return tile_launch_size<DT, kWeightGrad, false>(a, big, s);
 }
 
 hipError_t launch_tile_bf16(const TileArgs& a, int mode, int act, int big, hipStream_t s);
