@@ -441,16 +441,16 @@ MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 _torch = None
 _raw_stream = None  # device -> its current stream's handle, without building a Stream object
 _CODES = {}  # torch dtype -> moe_dtype
-_I32 = _U8 = None
+_I32 = _U8 = _F32 = _Tensor = None
 
 
 def _op_types() -> None:
-    global _torch, _raw_stream, _I32, _U8
+    global _torch, _raw_stream, _I32, _U8, _F32, _Tensor
     import torch
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
         (lambda device: torch.cuda.current_stream(device).cuda_stream)
     _CODES.update({torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16})
-    _I32, _U8 = torch.int32, torch.uint8
+    _I32, _U8, _F32, _Tensor = torch.int32, torch.uint8, torch.float32, torch.Tensor
     _torch = torch
 
 
@@ -461,19 +461,23 @@ def _op_code(t, name: str) -> int:
     return code
 
 
-def _op_ptrs(device: int, **tensors) -> list:
-    """Addresses of the given tensors (0 for None), each contiguous and on the device."""
+def _op_ptrs(device: int, names: str, *tensors) -> list:
+    """Addresses of the tensors (0 for None), each contiguous and on the device.  names: theirs, for a refusal."""
     out = []
-    for name, t in tensors.items():
+    for t in tensors:
         if t is None:
             out.append(0)
-            continue
-        if not isinstance(t, _torch.Tensor) or t.get_device() != device:
-            raise TypeError(f"{name} must be a tensor on the current device (cuda:{device})")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
+        elif isinstance(t, _Tensor) and t.get_device() == device and t.is_contiguous():
+            out.append(t.data_ptr())
+        else:
+            _op_refuse(device, names.split()[len(out)], t)
     return out
+
+
+def _op_refuse(device: int, name: str, t):
+    if not isinstance(t, _Tensor) or t.get_device() != device:
+        raise TypeError(f"{name} must be a tensor on the current device (cuda:{device})")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _op_device() -> int:
@@ -485,6 +489,8 @@ def _op_device() -> int:
 def _op_stream(device: int, stream) -> int:
     if stream is None:
         return _raw_stream(device)
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"stream must belong to the current device (cuda:{device})")
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -503,25 +509,29 @@ def _op_rows(slot_offsets, S: int, perm_pair, x, modes, k: int) -> int:
 
 def _op_matrix(t, cols: int, R: int, mode: int, k: int, name: str) -> None:
     need = -(-R // max(k, 1)) if mode == MOE_ROWS_TOKEN else R
-    if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < need:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected at least {need} rows of {cols}")
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or shape[0] < need:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected at least {need} rows of {cols}")
 
 
 def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: int = MOE_ROWS_POSITION,
                     y_rows: int = MOE_ROWS_POSITION, transpose: bool = False, act: int = MOE_ACT_NONE, stream=None):
     """y rows = x rows times their slot's matrix of w [S, N, K] (transposed unless `transpose`)."""
     dev = _op_device()
-    if w.dim() != 3 or not w[0].is_contiguous():
+    shape, strides = w.shape, w.stride()
+    if len(shape) != 3 or strides[2] != 1 or (strides[1] != shape[2] and shape[1] != 1):
         raise ValueError("w must be [S, N, K] with contiguous matrices")
-    S, N, K = w.shape
+    S, N, K = shape
     wide_in, wide_out = (N, K) if transpose else (K, N // 2 if act else N)
     R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
     _op_matrix(x, wide_in, R, x_rows, k, "x")
     _op_matrix(y, wide_out, R, y_rows, k, "y")
     if w.dtype != x.dtype:
         raise TypeError(f"w has dtype {w.dtype}, x {x.dtype}")
-    xp, wp, op, pp, yp = _op_ptrs(dev, x=x, w=w[0], slot_offsets=slot_offsets, perm_pair=perm_pair, y=y)
-    _check(lib().moe_expert_gemm(xp, _op_code(x, "x"), wp, 2 * (w.stride(0) if S > 1 else N * K), S, N, K,
+    xp, op, pp, yp = _op_ptrs(dev, "x slot_offsets perm_pair y", x, slot_offsets, perm_pair, y)
+    if w.get_device() != dev:
+        _op_refuse(dev, "w", w)
+    _check(lib().moe_expert_gemm(xp, _op_code(x, "x"), w.data_ptr(), 2 * (strides[0] if S > 1 else N * K), S, N, K,
                                  int(bool(transpose)), op, R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"),
                                  _op_stream(dev, stream)))
 
@@ -534,15 +544,16 @@ def moe_expert_gemm_wgrad(dy, x, slot_offsets, dw, perm_pair=None, k: int = 1, d
                           x_rows: int = MOE_ROWS_POSITION, ws=None, stream=None):
     """dw [S, N, K] = per slot, the sum over its positions of dy row (outer) x row."""
     dev = _op_device()
-    if dw.dim() != 3:
+    shape = dw.shape
+    if len(shape) != 3:
         raise ValueError("dw must be [S, N, K]")
-    S, N, K = dw.shape
+    S, N, K = shape
     R = _op_rows(slot_offsets, S, perm_pair, x, (dy_rows, x_rows), k)
     _op_matrix(dy, N, R, dy_rows, k, "dy")
     _op_matrix(x, K, R, x_rows, k, "x")
     if dy.dtype != x.dtype:
         raise TypeError(f"dy has dtype {dy.dtype}, x {x.dtype}")
-    dp, xp, op, pp, wp, sp = _op_ptrs(dev, dy=dy, x=x, slot_offsets=slot_offsets, perm_pair=perm_pair, dw=dw, ws=ws)
+    dp, xp, op, pp, wp, sp = _op_ptrs(dev, "dy x slot_offsets perm_pair dw ws", dy, x, slot_offsets, perm_pair, dw, ws)
     _check(lib().moe_expert_gemm_wgrad(dp, xp, _op_code(x, "x"), S, N, K, op, R, pp, k, dy_rows, x_rows, wp,
                                        _op_code(dw, "dw"), sp, 0 if ws is None else ws.numel() * ws.element_size(),
                                        _op_stream(dev, stream)))
@@ -553,9 +564,10 @@ def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pa
                        stream=None):
     """y rows = x rows times their slot's 4-bit matrix: codes q [S, N, K / 2], scales (and zeros) [S, N, K / group]."""
     dev = _op_device()
-    if q.dim() != 3 or q.dtype != _U8:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype != _U8:
         raise ValueError("q must be uint8 [S, N, K / 2]")
-    S, N, K = q.shape[0], q.shape[1], 2 * q.shape[2]
+    S, N, K = shape[0], shape[1], 2 * shape[2]
     if group < 1 or scales.shape != (S, N, K // group):
         raise ValueError(f"scales have shape {tuple(scales.shape)}, expected [{S}, {N}, K / group]")
     if zeros is not None and (zeros.dtype != _U8 or zeros.shape != scales.shape):
@@ -563,52 +575,55 @@ def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pa
     R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
     _op_matrix(x, K, R, x_rows, k, "x")
     _op_matrix(y, N // 2 if act else N, R, y_rows, k, "y")
-    xp, qp, sp, zp, op, pp, yp = _op_ptrs(dev, x=x, q=q, scales=scales, zeros=zeros, slot_offsets=slot_offsets,
-                                          perm_pair=perm_pair, y=y)
+    xp, qp, sp, zp, op, pp, yp = _op_ptrs(dev, "x q scales zeros slot_offsets perm_pair y", x, q, scales, zeros,
+                                          slot_offsets, perm_pair, y)
     _check(lib().moe_expert_gemv_w4(xp, _op_code(x, "x"), qp, sp, _op_code(scales, "scales"), zp, group, S, N, K, op,
                                     R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"), _op_stream(dev, stream)))
 
 
 def _norm_shapes(x, y, w_post, gate, w_pre) -> tuple:
-    """(T, H, gate mode, weight type) of a block norm's tensors."""
-    if x.dim() != 2 or (y is not None and y.shape != x.shape):
+    """(shape, gate mode, weight type) of a block norm's tensors."""
+    shape = x.shape
+    if len(shape) != 2 or (y is not None and y.shape != shape):
         raise ValueError("x and y must be [T, H] of one shape")
-    T, H = x.shape
-    w_dtype = None
+    T, H = shape
+    vector, first = (H,), None
     for name, w in (("w_post", w_post), ("w_pre", w_pre), ("gate", gate)):
         if w is None:
             continue
-        if w_dtype is None:
-            w_dtype = w.dtype
-        if w.dtype != w_dtype:
+        if first is None:
+            first = w.dtype
+        elif w.dtype != first:
             raise TypeError("w_post, gate and w_pre must have one dtype")
-        if name != "gate" and w.shape != (H,):
+        if name != "gate" and w.shape != vector:
             raise ValueError(f"{name} must be [{H}]")
     mode = MOE_GATE_NONE
     if gate is not None:
-        if gate.shape == (H,):
+        if gate.shape == vector:
             mode = MOE_GATE_CHANNEL
         elif gate.shape == (T, 1):
             mode = MOE_GATE_TOKEN
         else:
             raise ValueError(f"gate has shape {tuple(gate.shape)}, expected [{H}] (a channel's) or [{T}, 1] (a token's)")
-    first = w_post if w_post is not None else w_pre if w_pre is not None else gate
-    return T, H, mode, MOE_F32 if first is None else _op_code(first, "weights")
+    w = w_post if w_post is not None else w_pre if w_pre is not None else gate
+    return shape, mode, MOE_F32 if w is None else _op_code(w, "weights")
 
 
-def _norm_like(t, want, name: str) -> None:
-    if t is not None and (t.shape != want.shape or t.dtype != want.dtype):
-        raise ValueError(f"{name} must have shape {tuple(want.shape)} and dtype {want.dtype}")
+def _norm_like(t, shape, dtype, name: str) -> None:
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)} and dtype {dtype}")
 
 
 def moe_block_norm(x, y, w_post, gate, w_pre, x_out, h, eps: float, res_scale: float = 1.0, stream=None):
     """x_out = res_scale x + gate norm(y) w_post and h = norm(x_out) w_pre in one pass over the rows.  gate: [H] (one
     for each channel), [T, 1] (one for each token) or None; y, w_post, w_pre, x_out and h may be None."""
     dev = _op_device()
-    T, H, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
-    _norm_like(x_out, x, "x_out")
-    _norm_like(h, x, "h")
-    xp, yp, wp, gp, np_, op, hp = _op_ptrs(dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, x_out=x_out, h=h)
+    shape, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
+    T, H = shape
+    dtype = x.dtype
+    _norm_like(x_out, shape, dtype, "x_out")
+    _norm_like(h, shape, dtype, "h")
+    xp, yp, wp, gp, np_, op, hp = _op_ptrs(dev, "x y w_post gate w_pre x_out h", x, y, w_post, gate, w_pre, x_out, h)
     _check(lib().moe_block_norm(xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_,
                                 w_code, T, H, eps, res_scale, op, hp, _op_stream(dev, stream)))
 
@@ -621,18 +636,18 @@ def moe_block_norm_backward(x, y, w_post, gate, w_pre, dx_out, dh, dx, dy, dw_po
                             res_scale: float = 1.0, ws=None, stream=None):
     """The gradients of moe_block_norm's outputs with respect to x, y and the channel vectors (fp32)."""
     dev = _op_device()
-    T, H, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
-    _norm_like(dx_out, x, "dx_out")
-    _norm_like(dh, x, "dh")
-    _norm_like(dx, x, "dx")
+    shape, mode, w_code = _norm_shapes(x, y, w_post, gate, w_pre)
+    T, H = shape
+    for name, d in (("dx_out", dx_out), ("dh", dh), ("dx", dx)):
+        _norm_like(d, shape, x.dtype, name)
     if y is not None:
-        _norm_like(dy, y, "dy")
+        _norm_like(dy, shape, y.dtype, "dy")
     for name, d, w in (("dw_post", dw_post, w_post), ("dgate", dgate, gate), ("dw_pre", dw_pre, w_pre)):
-        if (d is None) != (w is None) or (d is not None and (d.dtype != _torch.float32 or d.shape != w.shape)):
+        if (d is None) != (w is None) or (d is not None and (d.dtype != _F32 or d.shape != w.shape)):
             raise ValueError(f"{name} must be float32 with the shape of its weight, and None without one")
     xp, yp, wp, gp, np_, op, hp, dxp, dyp, d0, d1, d2, sp = _op_ptrs(
-        dev, x=x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, dx_out=dx_out, dh=dh, dx=dx, dy=dy, dw_post=dw_post,
-        dgate=dgate, dw_pre=dw_pre, ws=ws)
+        dev, "x y w_post gate w_pre dx_out dh dx dy dw_post dgate dw_pre ws", x, y, w_post, gate, w_pre, dx_out, dh, dx,
+        dy, dw_post, dgate, dw_pre, ws)
     _check(lib().moe_block_norm_backward(
         xp, _op_code(x, "x"), yp, MOE_F32 if y is None else _op_code(y, "y"), wp, gp, mode, np_, w_code, T, H, eps,
         res_scale, op, hp, dxp, dyp, d0, d1, d2, sp, 0 if ws is None else ws.numel() * ws.element_size(),
@@ -640,12 +655,13 @@ def moe_block_norm_backward(x, y, w_post, gate, w_pre, dx_out, dh, dx, dy, dw_po
 
 
 def _swiglu_shapes(gu, slot_offsets, **halves) -> tuple:
-    if gu.dim() != 2 or gu.shape[1] % 2:
+    shape, dtype = gu.shape, gu.dtype
+    if len(shape) != 2 or shape[1] % 2:
         raise ValueError("gu must be [R, 2 I]")
-    R, I = gu.shape[0], gu.shape[1] // 2
+    R, I = shape[0], shape[1] // 2
     for name, t in halves.items():
-        if t is not None and (t.shape != (R, I) or t.dtype != gu.dtype):
-            raise ValueError(f"{name} must be [{R}, {I}] of dtype {gu.dtype}")
+        if t is not None and (t.dtype != dtype or t.shape != (R, I)):
+            raise ValueError(f"{name} must be [{R}, {I}] of dtype {dtype}")
     S = 0
     if slot_offsets is not None:
         if slot_offsets.dtype != _I32 or slot_offsets.dim() != 1:
@@ -658,7 +674,7 @@ def moe_swiglu(gu, h, slot_offsets=None, stream=None):
     """h [R, I] = silu(g) u of rows gu = [g | u]; with slot_offsets only the rows that a slot owns."""
     dev = _op_device()
     R, I, S = _swiglu_shapes(gu, slot_offsets, h=h)
-    gp, op, hp = _op_ptrs(dev, gu=gu, slot_offsets=slot_offsets, h=h)
+    gp, op, hp = _op_ptrs(dev, "gu slot_offsets h", gu, slot_offsets, h)
     _check(lib().moe_swiglu(gp, _op_code(gu, "gu"), R, I, op, S, hp, _op_stream(dev, stream)))
 
 
@@ -666,8 +682,8 @@ def moe_swiglu_backward(gu, dh, dgu, h=None, slot_offsets=None, stream=None):
     """dgu [R, 2 I] for given dh [R, I]; h is written again unless None."""
     dev = _op_device()
     R, I, S = _swiglu_shapes(gu, slot_offsets, dh=dh, h=h)
-    _norm_like(dgu, gu, "dgu")
-    gp, dp, op, up, hp = _op_ptrs(dev, gu=gu, dh=dh, slot_offsets=slot_offsets, dgu=dgu, h=h)
+    _norm_like(dgu, gu.shape, gu.dtype, "dgu")
+    gp, dp, op, up, hp = _op_ptrs(dev, "gu dh slot_offsets dgu h", gu, dh, slot_offsets, dgu, h)
     _check(lib().moe_swiglu_backward(gp, dp, _op_code(gu, "gu"), R, I, op, S, up, hp, _op_stream(dev, stream)))
 
 

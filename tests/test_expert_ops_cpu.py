@@ -190,6 +190,12 @@ class TestBinding:
         with pytest.raises(TypeError, match="current device"):
             Q.moe_swiglu(self.bf(4, 16), self.bf(4, 8))
 
+    def test_stream_of_another_device_is_refused(self):
+        from types import SimpleNamespace
+        assert Q._op_stream(0, SimpleNamespace(cuda_stream=16, device_index=0)) == 16
+        with pytest.raises(ValueError, match="current device"):
+            Q._op_stream(0, SimpleNamespace(cuda_stream=16, device_index=1))
+
     @pytest.mark.parametrize("kw,match", [
         (dict(x=(4, 24)), "x has shape"), (dict(y=(3, 8)), "y has shape"), (dict(y=(4, 16)), "y has shape"),
         (dict(off=(4,)), "slot_offsets"), (dict(x_rows=1), "perm_pair"), (dict(w=(8, 16)), r"\[S, N, K\]"),
