@@ -77,7 +77,7 @@ moe_status moe_expert_gemm(const void* x, int dtype, const void* w, size_t w_str
     if (w_stride < (size_t)N * K * 2)
         return fail(MOE_ERR_INVALID_ARGUMENT, "w_stride %zu is smaller than the matrix (%zu bytes)", w_stride,
                     (size_t)N * K * 2);
-    const qmoe::ExpertGemmArgs a{x,      w,      w_stride, dtype, N,      K, transpose, {slot_offsets, perm_pair, S, R, k},
+    const qmoe::ExpertGemmArgs a{x,      w,      w_stride, dtype, N,      K, transpose, qmoe::row_map(slot_offsets, perm_pair, S, R, k),
                                  x_rows, y_rows, act,      y,     y_dtype};
     return launched(qmoe::launch_expert_gemm(a, (hipStream_t)stream), "expert product launch");
 }
@@ -102,7 +102,7 @@ moe_status moe_expert_gemm_wgrad(const void* dy, const void* x, int dtype, int S
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", ws_bytes, need);
     if (need > 0 && (!ws || !aligned16(ws)))
         return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be non-NULL and 16-byte aligned");
-    const qmoe::ExpertWgradArgs a{dy, x, dtype, N, K, {slot_offsets, perm_pair, S, R, k}, dy_rows, x_rows,
+    const qmoe::ExpertWgradArgs a{dy, x, dtype, N, K, qmoe::row_map(slot_offsets, perm_pair, S, R, k), dy_rows, x_rows,
                                   dw, dw_dtype, ws};
     return launched(qmoe::launch_expert_wgrad(a, (hipStream_t)stream), "weight gradient launch");
 }
@@ -123,7 +123,7 @@ moe_status moe_expert_gemv_w4(const void* x, int dtype, const void* q, const voi
     if (!aligned16(x) || !aligned16(q) || !aligned16(scales) || !aligned16(y))
         return fail(MOE_ERR_INVALID_ARGUMENT, "x, q, scales and y must be 16-byte aligned");
     const qmoe::ExpertW4Args a{x, dtype, static_cast<const uint8_t*>(q), scales, scale_dtype, zeros, group, N, K,
-                               {slot_offsets, perm_pair, S, R, k}, x_rows, y_rows, act, y, y_dtype};
+                               qmoe::row_map(slot_offsets, perm_pair, S, R, k), x_rows, y_rows, act, y, y_dtype};
     return launched(qmoe::launch_expert_w4(a, (hipStream_t)stream), "4-bit product launch");
 }
 

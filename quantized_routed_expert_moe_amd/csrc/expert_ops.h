@@ -17,7 +17,13 @@ struct RowMap {
     const int32_t* offsets;  // [S + 1], or NULL: slot 0 owns all R positions
     const int32_t* perm;     // [R], or NULL
     int S, R, k;
+    // p / k = p inv_k >> 30 for p < 2^24 and k <= 64, with inv_k = 2^30 / k
+    // rounded up: the excess p (k - 1) / (k 2^30) stays below 1 / k.
+    uint32_t inv_k;
 };
+inline RowMap row_map(const int32_t* offsets, const int32_t* perm, int S, int R, int k) {
+    return {offsets, perm, S, R, k, ((1u << 30) + k - 1) / k};
+}
 
 struct ExpertGemmArgs {
     const void* x;
@@ -169,12 +175,15 @@ __device__ __forceinline__ int2 slot_range(const RowMap& m, int s) {
     return make_int2(a, max(b - a, 0));
 }
 
+// Token of pair p.
+__device__ __forceinline__ int token_of(const RowMap& m, int p) { return (int)__umulhi((uint32_t)p << 2, m.inv_k); }
+
 // Row of an operand for batch position q (q in [0, R)); the pair is clamped
 // to [0, R), so a bad permutation reads or writes inside the operand.
 __device__ __forceinline__ int row_of(const RowMap& m, int how, int q) {
     if (how == MOE_ROWS_POSITION) return q;
     const int p = min(max(m.perm[q], 0), m.R - 1);
-    return how == MOE_ROWS_PAIR ? p : p / m.k;
+    return how == MOE_ROWS_PAIR ? p : token_of(m, p);
 }
 
 // row_of in two parts: the pair (or position) as loaded, and its row.
@@ -183,7 +192,7 @@ __device__ __forceinline__ int pair_of(const RowMap& m, int how, int q) {
 }
 __device__ __forceinline__ int row_of_pair(const RowMap& m, int how, int p) {
     p = min(max(p, 0), m.R - 1);
-    return how == MOE_ROWS_TOKEN ? p / m.k : p;
+    return how == MOE_ROWS_TOKEN ? token_of(m, p) : p;
 }
 
 #endif  // __HIPCC__

@@ -47,9 +47,18 @@ struct StreamArgs {
 };
 
 constexpr int kSegment = 256;  // inputs a wave takes at a time
+// Groups of a row whose scales and zeros the workgroup holds in LDS (loaded by
+// the waves for each segment, a few bytes of 16 rows at a time, they took 13 %
+// of a pool's time).  The stride puts 16 rows on different banks.
+constexpr int kTableGroups = 64, kTableStride = kTableGroups + 2;
+// Rows up to which 4-bit products share out the loads of x.  With the table,
+// 192 experts of 4096 x 7168 for 256 pairs: 711 -> 530 us, 5.6 TB/s of codes,
+// scales and zeros.  (16-bit weights have four times the bytes a load of x:
+// no gain.)
+constexpr int kFewRows = 4;
 // Waves that split a workgroup's inputs.  Four: more would leave a CU one or
-// two workgroups (128 experts of 4096 x 7168 at 12 rows a slot takes 671
-// us, with eight 792 us).
+// two workgroups (128 4-bit experts of 4096 x 7168 take 368 us at 1.5 rows a
+// slot and 624 us at 12, with eight 429 and 807 us).
 constexpr int kStreamWaves = 4;
 
 template <int DT>
@@ -104,10 +113,11 @@ __device__ __forceinline__ T load_bytes(const uint8_t* p) {
     return v;
 }
 
-// The value that the first quarter's lane of the same lane % 16 holds.
-__device__ __forceinline__ uint32_t first_quarter(uint32_t v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    return __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false)[0];
+// Lane l of a row of 16 <- lane l + N.
+template <int N>
+__device__ __forceinline__ uint4 row_shift(uint4 v) {
+    auto one = [](uint32_t w) { return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w, 0x100 + N, 0xF, 0xF, true); };
+    return make_uint4(one(v.x), one(v.y), one(v.z), one(v.w));
 }
 
 // Slot of index i: with fewer positions than slots the i-th slot that owns
@@ -137,12 +147,14 @@ __device__ __forceinline__ int stream_slot(const RowMap& m, int i) {
     return -1;
 }
 
+// The launch bounds' second number keeps the sums in ordinary registers: the
+// accumulation registers would be read back one by one for the scales.
 // WT 0: 16-bit weights, 1: 4-bit.  SWI: tile 0 holds gate rows, tile 1 the up
 // rows of the same 16 features (NT = 2).
 template <int WT, int DT, int NT, int MB, int PER, bool SWI>
-__global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const StreamArgs a) {
+__global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 : 2) void expert_stream_kernel(const StreamArgs a) {
     typedef typename DType<DT>::type E;
-    extern __shared__ float red[];  // [waves][NT][MB][64][4]
+    extern __shared__ float red[];  // [waves][NT][MB][64][4]; before that the table of scales
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int col = lane & 15, c = lane >> 4;
     const int slot = __builtin_amdgcn_readfirstlane(stream_slot(a.rows, blockIdx.y));
@@ -152,219 +164,219 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
     const int n0 = blockIdx.x * (SWI ? 16 : 16 * NT);
     const uint8_t* w = static_cast<const uint8_t*>(a.w) + (size_t)slot * a.w_stride;
     const uint8_t* wp[NT];
-    size_t sp[NT];  // first scale of the lane's weight row
+    auto weight_row = [&](int row) {  // of the workgroup's 16 NT
+        return SWI ? min(n0 + row % 16, half - 1) + row / 16 * half : min(n0 + row, N - 1);
+    };
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int n = SWI ? min(n0 + col, half - 1) + t * half : min(n0 + 16 * t + col, N - 1);
-        wp[t] = w + (WT ? (size_t)n * (K / 2) : (size_t)n * K * 2);
-        sp[t] = WT ? ((size_t)slot * N + n) * (K >> a.group_shift) : 0;
-    }
+    for (int t = 0; t < NT; ++t) wp[t] = w + (size_t)weight_row(16 * t + col) * (WT ? K / 2 : K * 2);
+    // Scales and zeros of groups g0 to g0 + kTableGroups of the workgroup's
+    // rows, as fp32 pairs; a zero scale behind a row's end.
+    float2* table = reinterpret_cast<float2*>(red);
+    auto fill = [&](int g0) {
+        const int groups = K >> a.group_shift;
+        for (int u = threadIdx.x; u < 2 * NT * kTableGroups; u += blockDim.x) {
+            const int row = u / (kTableGroups / 8), at = u % (kTableGroups / 8) * 8, left = groups - g0 - at;
+            if (left <= 0) continue;
+            const size_t from = ((size_t)slot * N + weight_row(row)) * groups + g0 + at;
+            float2 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = make_float2(0.0f, 8.0f);
+            if (left >= 8) {
+                uint64_t z = 0;
+                if (a.zeros) z = load_bytes<uint64_t>(a.zeros + from);
+                if (a.scale_f32) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i].x = static_cast<const float*>(a.scales)[from + i];
+                } else {
+                    const uint4 v = load_bytes<uint4>(static_cast<const uint8_t*>(a.scales) + from * 2);
+                    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        q[i].x = (float)__builtin_bit_cast(E, (uint16_t)(h[i / 2] >> (16 * (i & 1))));
+                }
+                if (a.zeros)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i].y = (float)((uint32_t)(z >> (8 * i)) & 0xFFu);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 7; ++i) {
+                    if (i >= left) continue;
+                    q[i].x = a.scale_f32 ? static_cast<const float*>(a.scales)[from + i]
+                                         : (float)static_cast<const E*>(a.scales)[from + i];
+                    if (a.zeros) q[i].y = (float)a.zeros[from + i];
+                }
+            }
+            float4* to = reinterpret_cast<float4*>(table + row * kTableStride + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = make_float4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y);
+        }
+    };
     for (int rb = 0; rb < r.y; rb += 16 * MB) {
         const int nr = min(r.y - rb, 16 * MB);
-        // The lane's x rows: requested first, turned into addresses only behind
-        // the first weight loads, so that those do not wait for them.
-        int xrow[MB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) xrow[m] = pair_of(a.rows, a.x_rows, r.x + rb + min(16 * m + col, nr - 1));
         f32x4 tot[NT][MB] = {};
-        // A segment of 256 inputs: its weights, scales and zeros as loaded.
-        constexpr int LD = WT ? 2 : 8;        // 16-byte weight loads a tile
-        constexpr int SG = WT ? 8 / PER : 2;  // groups of the segment
-        constexpr int XI = MB == 4 ? 4 : 8;   // x instructions held at a time: 64 rows of eight would spill
-        typedef uint32_t s16v __attribute__((ext_vector_type(SG / 2)));
-        typedef uint32_t s32v __attribute__((ext_vector_type(SG)));
-        auto run = [&](auto scale_tag, auto zero_tag) {
-            constexpr bool SCALE_F32 = decltype(scale_tag)::value, ZEROS = decltype(zero_tag)::value;
-            struct Segment {
-                uint4 w[NT][LD];
-                s16v s16[NT];
-                s32v s32[NT];
-                uint64_t z[NT];
-            };
+        // A pass over the weights.  XR: rows that share one load of x.
+        auto pass = [&](auto xr_tag) {
+            constexpr int XR = decltype(xr_tag)::value;
+            constexpr bool FEW = XR == kFewRows;
+            constexpr int LD = WT ? 2 : 8;         // 16-byte weight loads a tile
+            constexpr int XI = MB == 4 ? 4 : 8;    // x instructions held at a time: 64 rows of eight would spill
+            constexpr int XL = FEW ? XR / 2 : XI;  // x loads of those
+            // The lane's x rows: requested first, turned into addresses only behind
+            // the first weight loads, so that those do not wait for them.
+            int xrow[MB];
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                xrow[m] = pair_of(a.rows, a.x_rows, r.x + rb + min(16 * m + (FEW ? col % XR : col), nr - 1));
+            typedef uint4 Weights[NT][LD];
+            typedef uint4 Xv[MB][XL];
             // CUT: the row's last segment, shorter than 256
-            auto load = [&](Segment& v, int k0, auto cut_tag) {
+            auto load = [&](Weights& v, int k0, auto cut_tag) {
                 constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
                 for (int i = 0; i < LD; ++i) {
                     const int k = WT ? k0 + 128 * i + 32 * c : k0 + 32 * i + 8 * c;
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        if (CUT) v.w[t][i] = make_uint4(0, 0, 0, 0);
-                        if (!CUT || k < K) v.w[t][i] = *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2));
-                    }
-                }
-                if constexpr (WT) {
-                    // A row's groups of the segment lie side by side: one load of
-                    // up to 16 bytes (2- or 1-byte aligned), since single values
-                    // cost the address unit a lane at a time.
-                    // The four quarters want the same values: the first loads them.
-                    auto at = [&](int t, int g) { return sp[t] + (min(k0 + 32 * PER * g, K - 1) >> a.group_shift); };
-                    if (CUT || c == 0)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if constexpr (SCALE_F32) {
-                            const uint32_t* p = static_cast<const uint32_t*>(a.scales);
-                            if (!CUT) __builtin_memcpy(&v.s32[t], p + at(t, 0), 4 * SG);
-                            else
-#pragma unroll
-                                for (int g = 0; g < SG; ++g) v.s32[t][g] = p[at(t, g)];
-                        } else {
-                            const uint16_t* p = static_cast<const uint16_t*>(a.scales);
-                            if (!CUT) __builtin_memcpy(&v.s16[t], p + at(t, 0), 2 * SG);
-                            else
-#pragma unroll
-                                for (int g = 0; g < SG; g += 2) v.s16[t][g / 2] = p[at(t, g)] | (uint32_t)p[at(t, g + 1)] << 16;
-                        }
-                        if constexpr (ZEROS) {
-                            v.z[t] = 0;
-                            if (!CUT) {
-                                if constexpr (SG == 2) v.z[t] = load_bytes<uint16_t>(a.zeros + at(t, 0));
-                                else if constexpr (SG == 4) v.z[t] = load_bytes<uint32_t>(a.zeros + at(t, 0));
-                                else v.z[t] = load_bytes<uint64_t>(a.zeros + at(t, 0));
-                            } else
-#pragma unroll
-                                for (int g = 0; g < SG; ++g) v.z[t] |= (uint64_t)a.zeros[at(t, g)] << (8 * g);
-                        }
+                        if (CUT) v[t][i] = make_uint4(0, 0, 0, 0);
+                        if (!CUT || k < K) v[t][i] = *reinterpret_cast<const uint4*>(wp[t] + (WT ? k / 2 : k * 2));
                     }
                 }
             };
-            uint4 xv[MB][XI];
-            // x fragments: instruction i takes the inputs that the weights'
-            // words hold; lanes of rows past the batch load nothing
-            auto load_x = [&](int k0, int i0, auto cut_tag) {
+            // x fragments: instruction i takes the inputs that the weights' words
+            // hold; lanes of rows past the batch load nothing (their rows of
+            // the sums are not stored).  Up to four rows: the lanes that have no
+            // row bring other instructions' inputs (lane col: row col % 4,
+            // instruction 4 j + col / 4), two loads a segment instead of eight of
+            // the same cost.
+            auto load_x = [&](Xv& xv, int k0, int i0, auto cut_tag) {
                 constexpr bool CUT = decltype(cut_tag)::value;
 #pragma unroll
                 for (int m = 0; m < MB; ++m) {
                     if (CUT)
 #pragma unroll
-                        for (int j = 0; j < XI; ++j) xv[m][j] = make_uint4(0, 0, 0, 0);
+                        for (int j = 0; j < XL; ++j) xv[m][j] = make_uint4(0, 0, 0, 0);
                     int row = xrow[m];
                     asm("" : "+v"(row));  // not hoisted above the weight loads
                     const E* xp = static_cast<const E*>(a.x) + (size_t)row_of_pair(a.rows, a.x_rows, row) * K;
-                    if (16 * m + col < nr) {
+                    if (FEW || 16 * m + col < nr) {
 #pragma unroll
-                        for (int j = 0; j < XI; ++j) {
-                            const int i = i0 + j;
+                        for (int j = 0; j < XL; ++j) {
+                            const int i = FEW ? 16 / XR * j + col / XR : i0 + j;
                             const int k = WT && PER == 4 ? k0 + 128 * (i / 4) + 32 * c + 8 * (i % 4) : k0 + 32 * i + 8 * c;
                             if (!CUT || k < K) xv[m][j] = *reinterpret_cast<const uint4*>(xp + k);
                         }
                     }
                 }
             };
-            // what stands between a segment's loads and its use
-            auto arrange = [&](Segment& v, auto cut_tag) {
-                if constexpr (WT && !decltype(cut_tag)::value) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        if constexpr (SCALE_F32) {
-#pragma unroll
-                            for (int g = 0; g < SG; ++g) v.s32[t][g] = first_quarter(v.s32[t][g]);
-                        } else {
-#pragma unroll
-                            for (int g = 0; g < SG / 2; ++g) v.s16[t][g] = first_quarter(v.s16[t][g]);
-                        }
-                        if constexpr (ZEROS) {
-                            const uint32_t lo = first_quarter((uint32_t)v.z[t]);
-                            const uint32_t hi = SG > 4 ? first_quarter((uint32_t)(v.z[t] >> 32)) : 0u;
-                            v.z[t] = (uint64_t)hi << 32 | lo;
-                        }
-                    }
-                }
-                if constexpr (WT && PER < 4) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < LD; ++i) v.w[t][i] = transpose_quarters(v.w[t][i]);
+            auto fragment = [&](const Xv& xv, int m, int i) {  // of instruction i (of those held)
+                if constexpr (FEW) {
+                    const uint4 v = xv[m][i / 4];
+                    return i % 4 == 0 ? v : i % 4 == 1 ? row_shift<4>(v) : i % 4 == 2 ? row_shift<8>(v) : row_shift<12>(v);
+                } else {
+                    return xv[m][i];
                 }
             };
             // x instructions i0 .. i0 + XI of a segment
-            auto multiply = [&](const Segment& v, int k0, int i0, auto cut_tag) {
-                constexpr bool CUT = decltype(cut_tag)::value;
+            auto multiply = [&](const Weights& v, Xv& xv, int k0, int i0, int c0) {
                 if constexpr (WT) {
                     const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
                     const uint4 ones = make_uint4(one, one, one, one);
+                    const int g0 = (k0 - c0) >> a.group_shift;
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
 #pragma unroll
-                        for (int j = 0; j < XI; ++j) xv[m][j] = codes_order(xv[m][j]);
+                        for (int j = 0; j < XL; ++j) xv[m][j] = codes_order(xv[m][j]);
 #pragma unroll
                     for (int g = i0 / PER; g < (i0 + XI) / PER; ++g) {
                         f32x4 acc[NT][MB] = {}, sx[MB] = {};
 #pragma unroll
                         for (int p = 0; p < PER; ++p) {
                             const int i = g * PER + p;
+                            uint4 xf[MB];
+#pragma unroll
+                            for (int m = 0; m < MB; ++m) xf[m] = fragment(xv, m, i - i0);
 #pragma unroll
                             for (int t = 0; t < NT; ++t) {
-                                const uint4 u = v.w[t][i / 4];
+                                const uint4 u = v[t][i / 4];
                                 const uint4 f = codes_frag<DT>(i % 4 == 0 ? u.x : i % 4 == 1 ? u.y : i % 4 == 2 ? u.z : u.w);
 #pragma unroll
-                                for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xv[m][i - i0], f, acc[t][m]);
+                                for (int m = 0; m < MB; ++m) acc[t][m] = mfma16<DT>(xf[m], f, acc[t][m]);
                             }
 #pragma unroll
-                            for (int m = 0; m < MB; ++m) sx[m] = mfma16<DT>(xv[m][i - i0], ones, sx[m]);
+                            for (int m = 0; m < MB; ++m) sx[m] = mfma16<DT>(xf[m], ones, sx[m]);
                         }
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            float sc;
-                            if constexpr (SCALE_F32) {
-                                sc = __uint_as_float(v.s32[t][g]);
-                            } else {
-                                const uint32_t h = v.s16[t][g / 2] >> (16 * (g & 1)) & 0xFFFFu;
-                                sc = DT == MOE_BF16 ? __uint_as_float(h << 16)
-                                                    : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
-                            }
-                            if (CUT && k0 + 32 * PER * g >= K) sc = 0.0f;
-                            const float z = ZEROS ? (float)((uint32_t)(v.z[t] >> (8 * g)) & 0xFFu) : 8.0f;
+                            const float2 q = table[(16 * t + col) * kTableStride + g0 + g];
 #pragma unroll
                             for (int m = 0; m < MB; ++m)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    tot[t][m][e] = fmaf(sc, fmaf(-z, sx[m][e], acc[t][m][e]), tot[t][m][e]);
+                                    tot[t][m][e] = fmaf(q.x, fmaf(-q.y, sx[m][e], acc[t][m][e]), tot[t][m][e]);
                         }
-                        if (MB == 4) __builtin_amdgcn_sched_barrier(0);  // a group at a time: hoisted fragments spill
+                        __builtin_amdgcn_sched_barrier(0);  // a group at a time: hoisted fragments spill
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < XI; ++j)
+                    for (int j = 0; j < XI; ++j) {
+                        uint4 xf[MB];
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) xf[m] = fragment(xv, m, j);
 #pragma unroll
                         for (int t = 0; t < NT; ++t)
 #pragma unroll
-                            for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xv[m][j], v.w[t][i0 + j], tot[t][m]);
+                            for (int m = 0; m < MB; ++m) tot[t][m] = mfma16<DT>(xf[m], v[t][i0 + j], tot[t][m]);
+                    }
                 }
             };
-            const int step = waves * kSegment;
-            int k0 = wave * kSegment;
-            // (Loading the next segment while this one multiplies costs a quarter
-            // of the waves their registers and gains nothing.)
-            for (; k0 + kSegment <= K; k0 += step) {
-                Segment now;
-                load(now, k0, std::false_type{});
-                load_x(k0, 0, std::false_type{});
-                arrange(now, std::false_type{});
+            auto segment = [&](Weights& v, Xv& xv, int k0, int c0, auto cut_tag) {
+                if constexpr (WT && PER < 4) {
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < LD; ++i) v[t][i] = transpose_quarters(v[t][i]);
+                }
 #pragma unroll
                 for (int i0 = 0; i0 < 8; i0 += XI) {
-                    if (i0) load_x(k0, i0, std::false_type{});
-                    multiply(now, k0, i0, std::false_type{});
+                    if (i0) load_x(xv, k0, i0, cut_tag);
+                    multiply(v, xv, k0, i0, c0);
                 }
+            };
+            const std::false_type whole;
+            const std::true_type cut;
+            const int step = waves * kSegment, span = WT ? kTableGroups << a.group_shift : K;
+            int k0 = wave * kSegment, c0 = 0;
+            while (true) {
+                if (WT) {
+                    fill(c0 >> a.group_shift);
+                    __syncthreads();
+                }
+                for (; k0 + kSegment <= K && k0 - c0 < span; k0 += step) {
+                    Weights now;
+                    Xv xv;
+                    load(now, k0, whole);
+                    load_x(xv, k0, 0, whole);
+                    segment(now, xv, k0, c0, whole);
+                }
+                if (!WT || K - c0 <= span) break;
+                c0 += span;
+                __syncthreads();
             }
             if (k0 < K) {
-                Segment now;
-                load(now, k0, std::true_type{});
-                load_x(k0, 0, std::true_type{});
-                arrange(now, std::true_type{});
-#pragma unroll
-                for (int i0 = 0; i0 < 8; i0 += XI) {
-                    if (i0) load_x(k0, i0, std::true_type{});
-                    multiply(now, k0, i0, std::true_type{});
-                }
+                Weights now;
+                Xv xv;
+                load(now, k0, cut);
+                load_x(xv, k0, 0, cut);
+                segment(now, xv, k0, c0, cut);
             }
         };
-        // one loop for each kind of scales and zeros: a branch on them between
-        // the loads costs a wait for what is in flight
-        if (WT && a.scale_f32 && a.zeros) run(std::true_type{}, std::true_type{});
-        else if (WT && a.scale_f32) run(std::true_type{}, std::false_type{});
-        else if (WT && a.zeros) run(std::false_type{}, std::true_type{});
-        else run(std::false_type{}, std::false_type{});
+        if constexpr (WT && MB == 1) {
+            if (nr <= kFewRows) pass(std::integral_constant<int, kFewRows>{});
+            else pass(std::integral_constant<int, 16>{});
+        } else {
+            pass(std::integral_constant<int, 16>{});
+        }
+        if (WT) __syncthreads();  // the sums take the table's place
         // join the waves' parts in wave order; element (row, col) of a block
         // sits at lane 16 (row / 4) + col, component row % 4
 #pragma unroll
@@ -395,7 +407,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void expert_stream_kernel(const 
 
 template <int WT, int DT, int NT, int PER, bool SWI>
 static hipError_t stream_launch_rows(const StreamArgs& a, int mb, dim3 grid, int waves, hipStream_t s) {
-    const size_t lds = (size_t)waves * NT * mb * 1024;
+    const size_t sums = (size_t)waves * NT * mb * 1024, table = WT ? 16 * NT * kTableStride * sizeof(float2) : 0;
+    const size_t lds = sums > table ? sums : table;
     if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
     else if (mb == 2 || PER == 1) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
     else if constexpr (PER > 1) expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
