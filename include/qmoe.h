@@ -22,6 +22,17 @@
  *   moe_expert_ffn_q6k
  *   moe_combine               weighted sum of the pairs (+ shared expert)
  *
+ * Beside the layer stand calls for experts that are not block-quantized and
+ * for what surrounds the layer in a transformer block, over the same batches:
+ *
+ *   moe_expert_gemm /         each slot's batch times its bf16 or fp16 matrix,
+ *   moe_expert_gemm_wgrad     forward and both gradients
+ *   moe_expert_gemv_w4        the forward product with 4-bit group-scaled
+ *                             weights
+ *   moe_block_norm(_backward) norm, gate, residual sum and next norm in one
+ *                             pass, and their gradients
+ *   moe_swiglu(_backward)     the activation between two products
+ *
  * Conventions for every call:
  *   - Pointers marked "device" are device (HBM) addresses, "host" are host
  *     addresses.  The caller allocates and owns every buffer, including the

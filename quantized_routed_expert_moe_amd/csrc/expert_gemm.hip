@@ -13,11 +13,17 @@ static int possible_slots(const RowMap& m) { return !m.offsets ? 1 : m.S < m.R ?
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
     const int slots = possible_slots(a.rows);
-    // Few rows a slot: the weights' stream bounds the call.  64 experts of 4096 x
-    // 2048 take 225 us streamed and 259 us tiled at 16 rows each, 313 and 266
-    // us at 48; one matrix of 2048 x 2048 takes 12.6 and 19.3 us at 64 rows, 23.1
-    // and 22.0 us at 128.
-    if (!a.transpose && (a.rows.R <= 24ll * slots || a.rows.R <= 64)) {
+    // Few rows a slot: the weights' stream bounds the call.  Up to how many the
+    // streaming kernel is the faster one depends on the tiles that the other
+    // would have.  Few leave CUs idle: one matrix of 2048 x 2048 takes 12.9
+    // streamed and 15.9 us tiled at 64 rows, 19.8 and 15.9 at 96; 8192 x 4096 27
+    // and 40 us at 32 rows, 41 and 41 at 64.  Enough of them read the weights as
+    // fast, and only their start and store count, as much as 12 stages of 64: 256
+    // slots of 1408 x 1408 take 183 and 204 us at 8 rows, 202 and 207 at 12; 128 of
+    // 1536 x 2048 with SwiGLU 156 and 137 us at 2, 188 and 142 at 16.
+    const long long tiles = (long long)slots * ((a.N + 127) / 128);
+    const int few = tiles <= 64 ? 48 : tiles <= 128 || a.K < 1536 ? 12 : 2;
+    if (!a.transpose && a.rows.R <= (long long)few * slots) {
         const StreamArgs t{a.x, a.w, a.w_stride, nullptr, nullptr, 0, 0, a.N, a.K, a.rows, a.x_rows, a.y_rows, a.y,
                            a.y_dtype == MOE_F32};
         return a.dtype == MOE_BF16 ? launch_stream_bf16(t, 0, a.act, s) : launch_stream_f16(t, 0, a.act, s);

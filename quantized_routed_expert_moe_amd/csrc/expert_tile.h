@@ -10,8 +10,8 @@
 // its A matrix, so a lane ends with four consecutive output columns of one
 // row and the epilogue packs them without shuffles.  256 x 256 by eight waves of
 // 128 x 64 where such tiles fill the chip, else 128 x 128 by four of 64 x 64.
-// Measured for 8192 x 8192 x 8192 (bf16): 1290 TFLOP/s forward, 1280 data
-// gradient; four waves of 128 x 128 and rings of more, shorter stages were
+// Measured for 8192 x 8192 x 8192 (bf16): 1340 TFLOP/s forward, 1350 data
+// gradient, 1300 weight gradient; four waves of 128 x 128 and rings of more, shorter stages were
 // slower, and two 256 x 128 tiles a CU as well.
 //
 // The contraction advances 64 a stage through two LDS buffers, filled by
@@ -55,6 +55,7 @@ struct TileArgs {
     void* y;
     int y_f32;
     int splits;       // weight gradient: parts of a slot's rows
+    int group;        // column tiles of a group
 };
 
 enum { kForward = 0, kDataGrad = 1, kWeightGrad = 2 };
@@ -485,12 +486,14 @@ __global__ __launch_bounds__(C::THREADS, C::QI * C::PI == 4 ? 2 : 1) void expert
     lds.row[1] = srow + C::WINDOW;
 
     const int N = a.N, K = a.K;
-    // The column tiles of a row tile run on one XCD (workgroup number modulo
-    // 8), which then serves the shared rows from its L2.
+    // Groups of neighbouring column tiles of a row tile run on one XCD
+    // (workgroup number modulo 8), which serves their rows from its L2; the
+    // groups go round the XCDs.
     const int width = C::MODE == kForward ? (C::SWI ? N / 2 : N) : K;  // columns of the output
-    const int ptiles = (width + C::COLS - 1) / C::COLS;
-    const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
-    const int p0 = (j % ptiles) * C::COLS, qt = (j / ptiles) * 8 + xcd;
+    const int ptiles = (width + C::COLS - 1) / C::COLS, pgroups = (ptiles + a.group - 1) / a.group;
+    const int j = blockIdx.x >> 3, group = j / a.group * 8 + (blockIdx.x & 7), pt = group % pgroups * a.group + j % a.group;
+    const int p0 = pt * C::COLS, qt = group / pgroups;
+    if (pt >= ptiles) return;
     int slot, q0, nq, c0 = 0, len;
     if (C::MODE == kWeightGrad) {
         const int ntiles = (N + C::BQ - 1) / C::BQ;
@@ -529,9 +532,17 @@ static hipError_t tile_launch(const TileArgs& a, hipStream_t s) {
     const long long qtiles = C::MODE == kWeightGrad
                                  ? (long long)((a.N + C::BQ - 1) / C::BQ) * a.rows.S * a.splits
                                  : a.rows.R / C::BQ + (a.rows.R < a.rows.S ? a.rows.R : a.rows.S);
-    const long long grid = (qtiles + 7) / 8 * 8 * ptiles;
+    // Few row tiles: groups of four column tiles and less, so that every XCD gets
+    // some (512 rows of one 8192 x 4096 matrix: 45 us, 76 with all columns of a
+    // row tile on one XCD; 8192 x 8192 x 8192: 821 and 870 us).  Many: up to 16,
+    // fewer XCDs then read a row (128 slots of 256 rows, 1536 x 2048: 226 us,
+    // 235 with four).
+    const long long most = qtiles >= 64 ? 16 : qtiles * ptiles >= 256 ? 4 : 1, groups = (ptiles + most - 1) / most;
+    TileArgs t = a;
+    t.group = (int)((ptiles + groups - 1) / groups);
+    const long long grid = (qtiles * ((ptiles + t.group - 1) / t.group) + 7) / 8 * 8 * t.group;
     if (grid > 0x7FFFFFFFll) return hipErrorInvalidConfiguration;
-    expert_tile_kernel<C><<<dim3((uint32_t)grid), C::THREADS, 0, s>>>(a);
+    expert_tile_kernel<C><<<dim3((uint32_t)grid), C::THREADS, 0, s>>>(t);
     return hipGetLastError();
 }
 
