@@ -5,6 +5,8 @@
 // codes or 2 N K of 16-bit weights) for a handful of rows.  A workgroup owns
 // 16 NT columns of one slot's product, its waves split K in segments of 256,
 // and one LDS sum joins them: no second launch, no atomics, a fixed order.
+// Measured for 16 experts of 1536 x 2048 with SwiGLU, a row each: bf16 20 us
+// (5.0 TB/s), 4-bit in groups of 64 9.4 us.
 //
 // v_mfma_f32_16x16x32 takes the rows of x as its A operand (up to 16 a
 // block, MB blocks) and 16 rows of w as its B operand: lane l holds eight

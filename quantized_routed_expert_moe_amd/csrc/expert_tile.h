@@ -11,8 +11,8 @@
 // row and the epilogue packs them without shuffles.  256 x 256 by eight waves of
 // 128 x 64 where such tiles fill the chip, else 128 x 128 by four of 64 x 64.
 // Measured for 8192 x 8192 x 8192 (bf16): 1340 TFLOP/s forward, 1350 data
-// gradient, 1300 weight gradient; four waves of 128 x 128 and rings of more, shorter stages were
-// slower, and two 256 x 128 tiles a CU as well.
+// gradient, 1300 weight gradient; four waves of 128 x 128, rings of more and
+// shorter stages and two 256 x 128 tiles a CU were slower.
 //
 // The contraction advances 64 a stage through two LDS buffers, filled by
 // global_load_lds_dwordx4 (no register staging).  A stage is four steps of 16;

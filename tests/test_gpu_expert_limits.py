@@ -88,6 +88,34 @@ def test_4_bit_zeros_of_a_whole_byte(group):
     check_sums(y.cpu(), want, mag, K, F32)
 
 
+@pytest.mark.parametrize("K,group", [(4128, 32), (8256, 64), (16512, 128)])
+@pytest.mark.parametrize("rows", [2, 12, 28, 70])
+def test_4_bit_rows_of_many_groups(K, group, rows):
+    """More groups than a workgroup holds at a time (64), and a short rest; all counts of rows a pass."""
+    N = 40
+    x, q = rand((rows, K), 1), torch.randint(0, 256, (1, N, K // 2), generator=torch.Generator().manual_seed(2), dtype=torch.uint8)
+    scales = rand((1, N, K // group), 3).abs()
+    zeros = torch.randint(0, 16, (1, N, K // group), generator=torch.Generator().manual_seed(4), dtype=torch.uint8)
+    want, _, mag = product(x, w4_matrix(q, scales, zeros, group), None, rows, None, 1, POS, POS, False, 0,
+                           w4_magnitude(q, scales, zeros, group))
+    y = torch.empty((rows, N), device="cuda")
+    Q.moe_expert_gemv_w4(x.cuda(), q.cuda(), scales.cuda(), zeros.cuda(), group, None, y)
+    check_sums(y.cpu(), want, mag, K, F32)
+
+
+@pytest.mark.parametrize("k", [1, 3, 7, 64])
+def test_token_rows_at_the_end_of_the_range(k):
+    """Pairs up to 2^24 - 1 find their token (pair / k) exactly."""
+    R, N, K = 1 << 24, 8, 8
+    tokens = -(-R // k)
+    x = torch.arange(tokens, device="cuda").remainder(251).to(BF).unsqueeze(1).repeat(1, K)
+    w = torch.eye(8, dtype=BF).unsqueeze(0).cuda()
+    perm = torch.arange(R - 1, -1, -1, dtype=torch.int32, device="cuda")
+    y = torch.empty((R, N), dtype=BF, device="cuda")
+    Q.moe_expert_gemm(x, w, None, y, perm, k, Q.MOE_ROWS_TOKEN, POS)
+    assert torch.equal(y, x[(perm.long() // k)])
+
+
 @pytest.mark.parametrize("rows", [7, 45])
 def test_4_bit_nan_and_infinity_stay_in_their_rows(rows):
     """A row with an infinity or a NaN gives no finite value; the rows beside it do not change."""
