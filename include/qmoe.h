@@ -514,7 +514,7 @@ moe_status moe_expert_gemm_wgrad(const void* dy, const void* x, int dtype, int S
  * zero for each run of `group` inputs of a row:
  *   w_s[n, j] = scales[s, n, j / group] * (code - zeros[s, n, j / group])
  * For decode steps: every matrix of a slot with positions is read once for
- * each 64 positions (groups of 32: 32 positions) that the slot owns.
+ * each 16, 32 or 64 positions that the slot owns (by the sizes of the call).
  *
  * q          device, [S, N, K / 2] bytes: element 2i of a row in the low
  *            nibble of byte i, 2i + 1 in its high nibble (codes 0..15).

@@ -54,13 +54,13 @@ constexpr int kSegment = 256;  // inputs a wave takes at a time
 // of a pool's time).  The stride puts 16 rows on different banks.
 constexpr int kTableGroups = 64, kTableStride = kTableGroups + 2;
 // Rows up to which 4-bit products share out the loads of x.  With the table,
-// 192 experts of 4096 x 7168 for 256 pairs: 711 -> 530 us, 5.6 TB/s of codes,
+// 192 experts of 4096 x 7168 for 256 pairs: 711 -> 521 us, 5.7 TB/s of codes,
 // scales and zeros.  (16-bit weights have four times the bytes a load of x:
 // no gain.)
 constexpr int kFewRows = 4;
 // Waves that split a workgroup's inputs.  Four: more would leave a CU one or
-// two workgroups (128 4-bit experts of 4096 x 7168 take 368 us at 1.5 rows a
-// slot and 624 us at 12, with eight 429 and 807 us).
+// two workgroups (128 4-bit experts of 4096 x 7168 take 353 us at 1.5 rows a
+// slot and 1044 us at 30, with eight 420 and 1229 us).
 constexpr int kStreamWaves = 4;
 
 template <int DT>
@@ -412,8 +412,8 @@ static hipError_t stream_launch_rows(const StreamArgs& a, int mb, dim3 grid, int
     const size_t sums = (size_t)waves * NT * mb * 1024, table = WT ? 16 * NT * kTableStride * sizeof(float2) : 0;
     const size_t lds = sums > table ? sums : table;
     if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else if (mb == 2 || PER == 1) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else if constexpr (PER > 1) expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else if (mb == 2) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    else if constexpr (PER > 1 && (NT == 1 || SWI)) expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
 }
 
@@ -422,17 +422,21 @@ static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
     const int slots = a.rows.offsets ? (a.rows.R < a.rows.S ? a.rows.R : a.rows.S) : 1;
     const int mean = (a.rows.R + slots - 1) / slots;
-    // Rows a pass: twice the mean and more, so that a slot above it still
-    // takes one pass over its weights; 64 rows of groups of 32 would spill.
-    const int mb = mean <= 8 || a.rows.R <= 16 ? 1 : mean <= 16 || a.rows.R <= 32 || PER == 1 ? 2 : 4;
+    const int width = act ? a.N / 2 : a.N, tiles = (width + 15) / 16;
+    const bool few = (long long)tiles * slots <= 512;
+    // Blocks of 16 rows a pass.  Fewer leave the CUs more waves, and another pass
+    // over a slot's weights finds them in the caches (4-bit, 64 slots of 4096 x
+    // 2048: 12 rows 97 us by one block, 116 by two; 30 rows 170 by two, 318 by
+    // four).  16-bit weights, twice to four times the bytes, want one pass rather
+    // (64 slots of 1536 x 1024, 12 rows: 44 and 40 us), and so do few workgroups,
+    // where a pass is latency (one matrix of 4096 x 4096, 64 rows: 23 us by two
+    // blocks, 20 by four; groups of 32 would spill).
+    const int mb = mean <= (WT ? 16 : 8) || a.rows.R <= 16 ? 1 : !few || a.rows.R <= 32 || PER == 1 ? 2 : 4;
     const int segs = (a.K + kSegment - 1) / kSegment, turns = (segs + kStreamWaves - 1) / kStreamWaves;
     const int waves = (segs + turns - 1) / turns;
-    const int width = act ? a.N / 2 : a.N;
-    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(a, mb, dim3((width + 15) / 16, slots), waves, s);
-    const int tiles = (width + 15) / 16;
-    // one tile a workgroup while that leaves CUs without one
-    if ((long long)tiles * slots <= 512)
-        return stream_launch_rows<WT, DT, 1, PER, false>(a, mb, dim3(tiles, slots), waves, s);
+    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(a, mb, dim3(tiles, slots), waves, s);
+    // one tile a workgroup where two would leave CUs without one
+    if (few) return stream_launch_rows<WT, DT, 1, PER, false>(a, mb, dim3(tiles, slots), waves, s);
     return stream_launch_rows<WT, DT, 2, PER, false>(a, mb, dim3((tiles + 1) / 2, slots), waves, s);
 }
 

@@ -1,6 +1,6 @@
 // Expert products with 4-bit group-scaled weights: the streaming kernels of
-// expert_stream.h at every row count (64 rows a slot share one pass over the
-// weights).
+// expert_stream.h at every row count (16, 32 or 64 rows a slot share one pass
+// over the weights).
 #include "expert_stream.h"
 
 namespace qmoe {
