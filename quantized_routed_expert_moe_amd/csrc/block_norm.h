@@ -309,10 +309,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_backward_ker
             raw_opaque<XT>(now.e[c]);
         }
         row_sum<TPR, 5>(sm, part, flip);
-        const float i2 = a.w_pre ? rsqrtf(sm[0] * inv + a.eps) : 0.0f;
-        const float m = i2 * sm[1] * inv;                        // mean(dn n)
-        const float sG = sm[2] + i2 * (sm[3] - i2 * m * sm[4]);  // sum(dxo G)
-        const float mp = now.g * sG * inv;                       // mean(dp p)
+        // Without a next norm no gradient holds x_out: its terms are left out, not
+        // taken times zero (x_out may be infinite, its sums may overflow).
+        const bool pre = a.w_pre != nullptr;
+        const float i2 = pre ? rsqrtf(sm[0] * inv + a.eps) : 0.0f;
+        const float m = pre ? i2 * sm[1] * inv : 0.0f;                               // mean(dn n)
+        const float sG = pre ? sm[2] + i2 * (sm[3] - i2 * m * sm[4]) : sm[2];        // sum(dxo G)
+        const float mp = now.g * sG * inv;                                           // mean(dp p)
         if (a.gate_mode == MOE_GATE_TOKEN && t == 0) a.dgate[row] = sG;
 #pragma unroll
         for (int c = 0; c < VPT; ++c) {
@@ -328,7 +331,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void block_norm_backward_ker
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float p = y[i] * i1, r = p * wpost[i];
-                const float n = fmaf(now.g, r * gate[i], a.res_scale * x[i]) * i2;
+                const float n = pre ? fmaf(now.g, r * gate[i], a.res_scale * x[i]) * i2 : 0.0f;
                 const float dxo = fmaf(i2, fmaf(e[i], wpre[i], -n * m), d[i]);
                 const float dr = dxo * gate[i] * now.g;
                 s_pre[c][i] = fmaf(e[i], n, s_pre[c][i]);
