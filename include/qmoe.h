@@ -524,7 +524,8 @@ moe_status moe_expert_gemm_wgrad(const void* dy, const void* x, int dtype, int S
  * N          a multiple of 8 (MOE_ACT_SWIGLU: of 16); N * K <= 2^30.
  * The other arguments as for moe_expert_gemm.  Codes and zeros enter exactly,
  * sums are fp32, y is rounded once.  A group's sums of code * x and of x are
- * kept apart, so an infinite x makes its row NaN.  q and scales are 16-byte
+ * kept apart, so an infinite x makes its row NaN.  They do not overflow for
+ * finite x; bf16 x below 2^-110 lose bits in them.  q and scales are 16-byte
  * aligned.
  */
 moe_status moe_expert_gemv_w4(const void* x, int dtype, const void* q, const void* scales, int scale_dtype,

@@ -17,8 +17,8 @@
 // they need for the dequantization.
 //
 // 4-bit weights: a byte 0..15 is the fp8 (e4m3) code of q / 512, so one
-// v_cvt_scalef32_pk_{bf16,f16}_fp8 with scale 512 turns two codes into two
-// exact 16-bit values: 7 instructions for 8 weights.  It yields elements
+// v_cvt_scalef32_pk_{bf16,f16}_fp8 scaled by 512 (and by kCodeUnit) turns two codes
+// into two exact 16-bit values: 7 instructions for 8 weights.  It yields elements
 // 0 2 4 6 1 3 5 7 of a word; the x fragments are put in that order (four byte
 // permutes for 16 rows x 8 inputs), the sum does not care.  With zero points
 //   sum_j s (q_j - z) x_j = s (sum_j q_j x_j - z sum_j x_j),
@@ -73,21 +73,30 @@ __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
                                                       0);
 }
 
-// Eight codes of a word -> elements 0 2 4 6 1 3 5 7 as exact 16-bit values.
+// What the codes and the ones against which x is summed are multiplied by: a
+// group's sums of code x and zero x reach 2^15 x, which for bf16 x near its
+// largest would overflow although scale (code - zero) x does not.  All of a row's
+// sums carry the factor, exactly but below 2^-110; the store takes it out.  fp16 x
+// has no such values.
+template <int DT> constexpr float kCodeUnit = DT == MOE_BF16 ? 1.0f / 65536.0f : 1.0f;
+
+// Eight codes of a word -> elements 0 2 4 6 1 3 5 7 as exact 16-bit values, times
+// kCodeUnit.
 template <int DT>
 __device__ __forceinline__ uint4 codes_frag(uint32_t w) {
     const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    constexpr float unit = 512.0f * kCodeUnit<DT>;
     uint4 f;
     if constexpr (DT == MOE_BF16) {
-        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, false));
-        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.0f, true));
-        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, false));
-        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.0f, true));
+        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, unit, false));
+        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, unit, true));
+        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, unit, false));
+        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, unit, true));
     } else {
-        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, false));
-        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 512.0f, true));
-        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, false));
-        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 512.0f, true));
+        f.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, unit, false));
+        f.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, unit, true));
+        f.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, unit, false));
+        f.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, unit, true));
     }
     return f;
 }
@@ -281,7 +290,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
             // x instructions i0 .. i0 + XI of a segment
             auto multiply = [&](const Weights& v, Xv& xv, int k0, int i0, int c0) {
                 if constexpr (WT) {
-                    const uint32_t one = DT == MOE_BF16 ? 0x3F803F80u : 0x3C003C00u;
+                    const uint32_t one = DT == MOE_BF16 ? 0x37803780u : 0x3C003C00u;  // kCodeUnit twice
                     const uint4 ones = make_uint4(one, one, one, one);
                     const int g0 = (k0 - c0) >> a.group_shift;
 #pragma unroll
@@ -398,6 +407,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
             }
             const int n = n0 + 16 * t + cc;
             if (n >= width) continue;
+            if (WT) v[0] *= 1.0f / kCodeUnit<DT>, v[1] *= 1.0f / kCodeUnit<DT>;
             if (SWI) v[0] = v[0] * sigmoid_f32(v[0]) * v[1];
             const size_t out = (size_t)row_of(a.rows, a.y_rows, r.x + rb + row) * width + n;
             if (a.y_f32) static_cast<float*>(a.y)[out] = v[0];
