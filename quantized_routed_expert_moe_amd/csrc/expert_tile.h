@@ -403,8 +403,9 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
             uint8_t* at = static_cast<uint8_t*>(a.y) + out * ES;
             // A weight gradient is not read again soon: past the caches it takes
             // 316 instead of 386 us (64 experts of 1536 x 2048, fp32, 280 to 2244
-            // rows each).
-            if (C::MODE == kWeightGrad)
+            // rows each).  Parts of one are, by the next launch (256 x 256, 32768 rows: 35.4
+            // us past the caches, 32.3 through them).
+            if (C::MODE == kWeightGrad && a.splits == 1)
                 __builtin_nontemporal_store(__builtin_bit_cast(u32x4, u), reinterpret_cast<u32x4*>(at));
             else
                 *reinterpret_cast<uint4*>(at) = u;
