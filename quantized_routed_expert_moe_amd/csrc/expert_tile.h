@@ -98,6 +98,7 @@ struct Tile {
     static constexpr bool QT = MODE == kWeightGrad, PT = MODE != kForward;  // transposed operands
     static constexpr int UQ = BQ / 8 / W, UP = BP / 8 / W;  // 1 KB loads of a wave for a stage
     static constexpr int QBYTES = BQ * 2 * BK, PBYTES = BP * 2 * BK;
+    static constexpr bool PARTS = MODE == kWeightGrad && BQ == 128;  // 256 x 256 tiles do not split a slot's rows
     static constexpr int COLS = SWI ? BP / 2 : BP;  // output columns of a tile
     static constexpr int WINDOW = 1024;             // weight gradient: source rows held in LDS
     static_assert(W % 2 == 0, "a load's rows keep their place in the swizzle");
@@ -372,8 +373,10 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
         if (v >= u * PERP && v < (u + 1) * PERP) mine = lds.p[u] + (v - u * PERP) * SHARE;
     }
     __syncthreads();
-    auto block = [&](auto f32_tag, int base, const f32x16 (&v)[PI], int p) {
-        constexpr bool F32 = decltype(f32_tag)::value;
+    // PAST: stored past the caches.  Known to the compiler: of a store with and one
+    // without the hint behind a branch it makes one without.
+    auto block = [&](auto f32_tag, auto past_tag, int base, const f32x16 (&v)[PI], int p) {
+        constexpr bool F32 = decltype(f32_tag)::value, PAST = decltype(past_tag)::value;
         constexpr int ES = F32 ? 4 : 2;
         // 128 bytes of a row: 32 fp32 columns, or the wave's 64 of a 16-bit type (SwiGLU leaves it 32)
         constexpr int BLOCKS = F32 || C::SWI ? 1 : 2, WIDE = 32 * BLOCKS, STRIDE = WIDE * ES + 16;
@@ -405,24 +408,26 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
             // 316 instead of 386 us (64 experts of 1536 x 2048, fp32, 280 to 2244
             // rows each).  Parts of one are, by the next launch (256 x 256, 32768 rows: 35.4
             // us past the caches, 32.3 through them).
-            if (C::MODE == kWeightGrad && a.splits == 1)
+            if constexpr (PAST)
                 __builtin_nontemporal_store(__builtin_bit_cast(u32x4, u), reinterpret_cast<u32x4*>(at));
             else
                 *reinterpret_cast<uint4*>(at) = u;
         }
     };
+    auto rows = [&](auto f32_tag, auto past_tag) {
+        constexpr int STEP = decltype(f32_tag)::value && !C::SWI ? 1 : 2;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const int base = 32 * (wq + WQ * b);
-        if (base >= nq) continue;
-        if (!a.y_f32) {
+        for (int b = 0; b < NB; ++b) {
+            const int base = 32 * (wq + WQ * b);
+            if (base >= nq) continue;
 #pragma unroll
-            for (int p = 0; p < PI; p += 2) block(std::false_type{}, base, acc[b], p);
-        } else {
-#pragma unroll
-            for (int p = 0; p < PI; p += C::SWI ? 2 : 1) block(std::true_type{}, base, acc[b], p);
+            for (int p = 0; p < PI; p += STEP) block(f32_tag, past_tag, base, acc[b], p);
         }
-    }
+    };
+    const std::bool_constant<C::MODE == kWeightGrad> past;
+    if (!a.y_f32) rows(std::false_type{}, past);
+    else if (C::PARTS && a.splits > 1) rows(std::true_type{}, std::false_type{});
+    else rows(std::true_type{}, past);
 }
 
 // Row tile `index` of the batch, slots in order: whole tiles (bound by the
