@@ -73,8 +73,16 @@ hipError_t launch_expert_wgrad(const ExpertWgradArgs& a, hipStream_t s) {
     t.splits = wgrad_splits(a.rows.S, a.N, a.K, a.rows.R);
     t.y = t.splits > 1 ? a.ws : a.dw;
     t.y_f32 = t.splits > 1 || a.dw_dtype == MOE_F32;
+    // 256 x 256 tiles where they fill the CUs and the products count as much as the
+    // store of dw, else 128 x 128, of which more share a CU.  128 slots of 1408 x 2048,
+    // us by large and by small tiles, fp32: 264 and 224 at a mean of half a row, 254 and
+    // 231 at 32, 346 and 335 at 128, 378 and 512 at 256; bf16: 130 and 120 at 4, 118 and
+    // 134 at 16.  Rows that end inside a line of 128 bytes cost large tiles more: 60 of
+    // 1072 x 1448, fp32: 186 and 83 at 16, 178 and 170 at 256; bf16 93 and 97 at 192.
+    const size_t row = (size_t)a.K * (a.dw_dtype == MOE_F32 ? 4 : 2);
+    const int few = row % 128 ? 192 : a.dw_dtype == MOE_F32 ? 32 : 8;
     const long long tiles = (long long)a.rows.S * ((a.N + 255) / 256) * ((a.K + 255) / 256);
-    const int big = t.splits == 1 && tiles >= 256;
+    const int big = t.splits == 1 && tiles >= 256 && a.rows.R > (long long)few * a.rows.S;
     const hipError_t e = a.dtype == MOE_BF16 ? launch_tile_bf16(t, kWeightGrad, 0, big, s)
                                              : launch_tile_f16(t, kWeightGrad, 0, big, s);
     if (e != hipSuccess || t.splits == 1) return e;

@@ -98,7 +98,6 @@ struct Tile {
     static constexpr bool QT = MODE == kWeightGrad, PT = MODE != kForward;  // transposed operands
     static constexpr int UQ = BQ / 8 / W, UP = BP / 8 / W;  // 1 KB loads of a wave for a stage
     static constexpr int QBYTES = BQ * 2 * BK, PBYTES = BP * 2 * BK;
-    static constexpr bool PARTS = MODE == kWeightGrad && BQ == 128;  // 256 x 256 tiles do not split a slot's rows
     static constexpr int COLS = SWI ? BP / 2 : BP;  // output columns of a tile
     static constexpr int WINDOW = 1024;             // weight gradient: source rows held in LDS
     static_assert(W % 2 == 0, "a load's rows keep their place in the swizzle");
@@ -149,6 +148,18 @@ __device__ __forceinline__ void spread() {
     }
 }
 
+// Fragment of a transposed operand of `width` columns: step of 16 of the
+// contraction, block of 32 columns from `col` on.
+__device__ __forceinline__ uint4 read_transposed(const uint8_t* s, int lane, int col, int step, int width) {
+    const int row = 8 * (lane >> 5) + ((lane & 15) >> 2);  // first contraction row of the read
+    const int chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int at = (16 * step + row) * width * 2 + (((col / 8 + chunk) ^ (4 * (row & 3))) * 16) + (lane & 1) * 8;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + at));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + at + 4 * width * 2));
+    const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
+    return make_uint4(l.x, l.y, h.x, h.y);
+}
+
 template <typename C>
 struct TileLds {
     uint8_t* q[C::NBUF];
@@ -197,7 +208,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
             po[i] = ((uint32_t)n * (uint32_t)K + 8 * dchunk) * 2;
         }
     }
-    const int stages = max((len + BK - 1) / BK, 4);  // the last of four may hold zeros only
+    const int stages = max((len + BK - 1) / BK, 4);  // the last three may hold zeros only
     // weight gradient: source rows of dy and x, a ring that is filled half a
     // window at a time well ahead of the loads
     int filled = 0;
@@ -263,29 +274,20 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
 
     // ---- fragment reads: step of 16, block of 32 rows or columns
     const int khalf = lane >> 5, swz = (lane >> 1) & 7;
-    const int trow = 8 * khalf + ((lane & 15) >> 2);  // first contraction row of a transposed read
-    const int tcol = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
     auto direct = [&](const uint8_t* s, int row, int step) {
         return *reinterpret_cast<const uint4*>(s + (row + (lane & 31)) * 128 + (((2 * step + khalf) ^ swz) * 16));
-    };
-    auto transposed = [&](const uint8_t* s, int col, int step, int width) {
-        const int at = (16 * step + trow) * width * 2 + (((col / 8 + tcol) ^ (4 * (trow & 3))) * 16) + (lane & 1) * 8;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + at));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(s + at + 4 * width * 2));
-        const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
-        return make_uint4(l.x, l.y, h.x, h.y);
     };
     uint4 fq[2][NB], fp[2][PI];
     auto read = [&](int set, int buf, int step) {
 #pragma unroll
         for (int p = 0; p < PI; ++p) {
             const int col = 32 * (wp * PI + p);
-            fp[set][p] = C::PT ? transposed(lds.p[buf], col, step, C::BP) : direct(lds.p[buf], col, step);
+            fp[set][p] = C::PT ? read_transposed(lds.p[buf], lane, col, step, C::BP) : direct(lds.p[buf], col, step);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const int row = 32 * (wq + WQ * b);
-            fq[set][b] = C::QT ? transposed(lds.q[buf], row, step, C::BQ) : direct(lds.q[buf], row, step);
+            fq[set][b] = C::QT ? read_transposed(lds.q[buf], lane, row, step, C::BQ) : direct(lds.q[buf], row, step);
         }
     };
     auto multiply = [&](int set) {
@@ -295,8 +297,7 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
             for (int p = 0; p < PI; ++p) acc[b][p] = mfma32<C::DT>(fp[set][p], fq[set][b], acc[b][p]);
     };
     constexpr int READS = (C::PT ? 2 : 1) * PI + (C::QT ? 2 : 1) * NB;
-    if (len <= 0) return;
-    if (MODE == kWeightGrad) fill_rows(C::WINDOW);
+    if (MODE == kWeightGrad) fill_rows(min(C::WINDOW, stages * BK));
     enum { kWhole, kRest, kNext, kLast };
     // Steps 0 to 3 of a stage.  kWhole, kRest: stage st + 2 exists, its loads
     // stand between the last step's matrix instructions.  kLast: nothing follows.
@@ -355,6 +356,61 @@ __device__ __forceinline__ void tile_product(const TileArgs& a, int slot, int q0
     stage(st + 3, 1, std::integral_constant<int, kLast>{});
 }
 
+// A weight gradient tile of a slot with at most 64 rows: one stage, and of it
+// only the steps of 16 rows that exist; a lane loads its row numbers itself.
+template <typename C>
+__device__ __forceinline__ void tile_short(const TileArgs& a, int q0, int c0, int p0, int len, const TileLds<C>& lds,
+                                           f32x16 (&acc)[C::QI][C::PI]) {
+    constexpr int W = C::W;
+    static_assert(16 * C::UQ == C::BK && 16 * C::UP == C::BK, "a load of every wave brings a step");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wq = wave % C::WQ, wp = wave / C::WQ, steps = (len + 15) / 16;
+    const uint8_t* zero = reinterpret_cast<const uint8_t*>(kZeroChunk);
+    const uint8_t* q = static_cast<const uint8_t*>(a.q) + (size_t)min(q0 + 8 * tr_chunk<C::BQ, W>(wave, lane), a.N - 8) * 2;
+    const uint8_t* p = static_cast<const uint8_t*>(a.p) + (size_t)min(p0 + 8 * tr_chunk<C::BP, W>(wave, lane), a.K - 8) * 2;
+#pragma unroll
+    for (int i = 0; i < C::UQ; ++i) {
+        if (i >= steps) continue;
+        const int rq = tr_row<C::BQ, W>(wave, lane, i), rp = tr_row<C::BP, W>(wave, lane, i);
+        const size_t from = (size_t)(uint32_t)row_of(a.rows, a.q_rows, c0 + min(rq, len - 1)) * (uint32_t)(a.N * 2);
+        load_to_lds(rq < len ? q + from : zero, lds.q[0] + (wave + W * i) * 1024);
+        const size_t with = (size_t)(uint32_t)row_of(a.rows, a.p_rows, c0 + min(rp, len - 1)) * (uint32_t)(a.K * 2);
+        load_to_lds(rp < len ? p + with : zero, lds.p[0] + (wave + W * i) * 1024);
+    }
+    wait_loads<0>();
+    __syncthreads();
+#pragma unroll
+    for (int step = 0; step < C::BK / 16; ++step) {
+        if (step >= steps) continue;
+        uint4 fq[C::QI], fp[C::PI];
+#pragma unroll
+        for (int b = 0; b < C::QI; ++b) fq[b] = read_transposed(lds.q[0], lane, 32 * (wq + C::WQ * b), step, C::BQ);
+#pragma unroll
+        for (int p = 0; p < C::PI; ++p) fp[p] = read_transposed(lds.p[0], lane, 32 * (wp * C::PI + p), step, C::BP);
+#pragma unroll
+        for (int b = 0; b < C::QI; ++b)
+#pragma unroll
+            for (int p = 0; p < C::PI; ++p) acc[b][p] = mfma32<C::DT>(fp[p], fq[b], acc[b][p]);
+    }
+}
+
+// Weight gradient of a slot (or part) without rows: tile `tile` of `tiles` writes
+// its share of the matrix's zeros, each wave one run of them.  128 slots of 1408 x
+// 2048 with 8 rows in all (small tiles), fp32 and bf16: 224 and 114 us, 6.6 and 6.5
+// TB/s; a workgroup's runs in turn 249 and 112 us, the tiles' own rows 230 and 120.
+// Odd widths gain most: 128 of 2064 x 472, bf16, 39 us, by the tiles' rows 87 us.
+template <typename C>
+__device__ __forceinline__ void tile_zero(const TileArgs& a, int slot, int tile, int tiles) {
+    const size_t units = (size_t)a.N * a.K / (a.y_f32 ? 4 : 8);  // of 16 bytes
+    const size_t share = ((units + tiles - 1) / tiles + 63) & ~(size_t)63;
+    const size_t from = min(units, tile * share), end = min(units, from + share), run = (end - from) / (C::W * 64) * 64;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const size_t to = wave == C::W - 1 ? end : from + (wave + 1) * run;
+    u32x4* y = static_cast<u32x4*>(a.y) + slot * units;
+    const u32x4 zero = {0, 0, 0, 0};
+    for (size_t i = from + wave * run + lane; i < to; i += 64) __builtin_nontemporal_store(zero, y + i);
+}
+
 // The tile's rows, rounded and stored: a block of 32 rows at a time through
 // the wave's share of the stage buffers, out in 16-byte pieces of whole rows.
 template <typename C, int NB>
@@ -404,10 +460,6 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
             const size_t out = C::MODE == kWeightGrad ? ((size_t)slot * N + q0 + row) * K + c
                                                       : (size_t)row_of(a.rows, a.y_rows, q0 + row) * width + c;
             uint8_t* at = static_cast<uint8_t*>(a.y) + out * ES;
-            // A weight gradient is not read again soon: past the caches it takes
-            // 316 instead of 386 us (64 experts of 1536 x 2048, fp32, 280 to 2244
-            // rows each).  Parts of one are, by the next launch (256 x 256, 32768 rows: 35.4
-            // us past the caches, 32.3 through them).
             if constexpr (PAST)
                 __builtin_nontemporal_store(__builtin_bit_cast(u32x4, u), reinterpret_cast<u32x4*>(at));
             else
@@ -424,10 +476,23 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
             for (int p = 0; p < PI; p += STEP) block(f32_tag, past_tag, base, acc[b], p);
         }
     };
-    const std::bool_constant<C::MODE == kWeightGrad> past;
-    if (!a.y_f32) rows(std::false_type{}, past);
-    else if (C::PARTS && a.splits > 1) rows(std::true_type{}, std::false_type{});
-    else rows(std::true_type{}, past);
+    // A weight gradient is not read again soon: past the caches it takes 287
+    // instead of 358 us (64 experts of 1536 x 2048, fp32, 280 to 2244 rows each).
+    // Small tiles go through the caches where a row ends inside a line of 128
+    // bytes, which would be written in two pieces (60 of 1072 x 1448, fp32, 27
+    // rows each: 158 us past, 100 through; 128 of 1408 x 2048, 4 rows each: 221 us
+    // past, 253 through), and with the parts that the next launch joins (256 x 256,
+    // 32768 rows: 35.4 us past, 32.3 through).
+    const std::true_type yes;
+    const std::false_type no;
+    if constexpr (C::MODE == kWeightGrad && C::BQ == 128) {
+        const bool past = a.splits == 1 && K * (a.y_f32 ? 4 : 2) % 128 == 0;
+        if (!a.y_f32) past ? rows(no, yes) : rows(no, no);
+        else past ? rows(yes, yes) : rows(yes, no);
+    } else {
+        const std::bool_constant<C::MODE == kWeightGrad> past;
+        a.y_f32 ? rows(yes, past) : rows(no, past);
+    }
 }
 
 // Row tile `index` of the batch, slots in order: whole tiles (bound by the
@@ -513,6 +578,12 @@ __global__ __launch_bounds__(C::THREADS, C::QI * C::PI == 4 ? 2 : 1) void expert
         c0 = r.x + min(part * per, r.y);
         len = min(per, r.x + r.y - c0);
         slot += part * a.rows.S;
+        if (len <= 0) return tile_zero<C>(a, slot, st % ntiles * ptiles + pt, ntiles * ptiles);
+        if (len <= C::BK) {
+            f32x16 acc[C::QI][C::PI] = {};
+            tile_short<C>(a, q0, c0, p0, len, lds, acc);
+            return tile_store<C, C::QI>(a, slot, q0, nq, p0, lds, acc);
+        }
     } else {
         if (!find_tile<C::BQ, C::THREADS>(a.rows, qt, slot, q0, nq)) return;
         len = C::MODE == kForward ? K : N;
