@@ -431,7 +431,10 @@ def moe_layer_decode(fmt: int, logits, x, k: int, score: int, renormalize: bool,
 # ------------------------------------- expert products, block norms, SwiGLU
 # These calls take their sizes from the tensors' shapes and check every shape
 # that a kernel relies on.  All tensors live on the current device, on whose
-# current stream (or `stream`) the call is enqueued.
+# current stream (or `stream`) the call is enqueued.  No call records itself for
+# autograd: with gradients enabled a tensor that requires one is refused (call
+# under torch.no_grad(), or from a torch.autograd.Function whose backward makes
+# the gradient calls).
 
 MOE_F16 = 2
 MOE_ROWS_POSITION, MOE_ROWS_PAIR, MOE_ROWS_TOKEN = 0, 1, 2
@@ -463,11 +466,11 @@ def _op_code(t, name: str) -> int:
 
 def _op_ptrs(device: int, names: str, *tensors) -> list:
     """Addresses of the tensors (0 for None), each contiguous and on the device.  names: theirs, for a refusal."""
-    out = []
+    out, grad = [], _torch.is_grad_enabled()
     for t in tensors:
         if t is None:
             out.append(0)
-        elif isinstance(t, _Tensor) and t.get_device() == device and t.is_contiguous():
+        elif isinstance(t, _Tensor) and t.get_device() == device and t.is_contiguous() and not (grad and t.requires_grad):
             out.append(t.data_ptr())
         else:
             _op_refuse(device, names.split()[len(out)], t)
@@ -477,6 +480,9 @@ def _op_ptrs(device: int, names: str, *tensors) -> list:
 def _op_refuse(device: int, name: str, t):
     if not isinstance(t, _Tensor) or t.get_device() != device:
         raise TypeError(f"{name} must be a tensor on the current device (cuda:{device})")
+    if t.requires_grad and _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: call it under torch.no_grad() or "
+                         "from a torch.autograd.Function")
     raise ValueError(f"{name} must be contiguous")
 
 
@@ -529,7 +535,7 @@ def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: i
     if w.dtype != x.dtype:
         raise TypeError(f"w has dtype {w.dtype}, x {x.dtype}")
     xp, op, pp, yp = _op_ptrs(dev, "x slot_offsets perm_pair y", x, slot_offsets, perm_pair, y)
-    if w.get_device() != dev:
+    if w.get_device() != dev or (w.requires_grad and _torch.is_grad_enabled()):
         _op_refuse(dev, "w", w)
     _check(lib().moe_expert_gemm(xp, _op_code(x, "x"), w.data_ptr(), 2 * (strides[0] if S > 1 else N * K), S, N, K,
                                  int(bool(transpose)), op, R, pp, k, x_rows, y_rows, act, yp, _op_code(y, "y"),
