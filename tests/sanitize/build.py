@@ -1,6 +1,6 @@
 """Builds the host-side sanitizer driver (driver.cpp) with AddressSanitizer
 and UndefinedBehaviorSanitizer: the driver, the C ABI's host code
-(csrc/abi.cpp, its device code unsanitized), the host leg and residency
+(csrc/abi.cpp and csrc/abi_ops.cpp, device code unsanitized), the host leg and residency
 policy, the oracle and the input generator are instrumented; the other HIP
 objects of the library build are linked as they are.  Output:
 _build/sanitize/driver.  CPU only; run by tests/test_sanitizers.py."""
@@ -37,13 +37,14 @@ def build() -> str:
     inc = ["-I" + os.path.join(ROOT, "include")]
     objs = []
     # the C ABI's host code, instrumented (device code as in the library)
-    abi = os.path.join(OUT, "abi.o")
-    _run([B.HIPCC, *[f for f in B.FLAGS if f not in ("-O3",)], *SAN_HOST_ONLY, "-x", "hip", "-c",
-          os.path.join(csrc, "abi.cpp"), "-o", abi])
-    objs.append(abi)
+    for src in ("abi.cpp", "abi_ops.cpp"):
+        obj = os.path.join(OUT, os.path.splitext(src)[0] + ".o")
+        _run([B.HIPCC, *[f for f in B.FLAGS if f not in ("-O3",)], *SAN_HOST_ONLY, "-x", "hip", "-c",
+              os.path.join(csrc, src), "-o", obj])
+        objs.append(obj)
     for src, lang in ((os.path.join(ROOT, "oracle", "oracle.c"), "c"), (os.path.join(ROOT, "fixtures", "fixtures.c"), "c"),
                       (os.path.join(host, "host_leg.cpp"), "c++"), (os.path.join(host, "residency.cpp"), "c++"),
-                      (os.path.join(HERE, "driver.cpp"), "c++")):
+                      (os.path.join(HERE, "driver.cpp"), "c++"), (os.path.join(HERE, "driver_ops.cpp"), "c++")):
         obj = os.path.join(OUT, os.path.basename(src) + ".o")
         cc = os.path.join(LLVM, "clang" if lang == "c" else "clang++")
         std = "-std=c11" if lang == "c" else "-std=c++17"
@@ -51,7 +52,7 @@ def build() -> str:
         objs.append(obj)
     # the library's other objects, as built by the package build
     for src in B.SOURCES:
-        if src == "abi.cpp":
+        if src in ("abi.cpp", "abi_ops.cpp"):
             continue
         obj = os.path.join(B.BUILD, os.path.splitext(src)[0] + ".o")
         if not os.path.exists(obj):

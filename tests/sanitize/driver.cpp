@@ -25,6 +25,8 @@ void fx_logits_normal(uint32_t seed, uint32_t layer, int64_t T, int E, float* ou
 void fx_logits_zipf(uint32_t seed, uint32_t perm_seed, uint32_t layer, int64_t T, int E, double s, float* out);
 }
 
+int driver_ops();  // driver_ops.cpp: failed checks
+
 static int g_failures = 0;
 #define CHECK(cond)                                                             \
     do {                                                                        \
@@ -253,6 +255,7 @@ int main() {
     pack_round_trips();
     slot_maps();
     refusals();
+    g_failures += driver_ops();
     host_leg();
     residency();
     oracle_layer();
