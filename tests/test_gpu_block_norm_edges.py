@@ -1,11 +1,12 @@
-"""Block norms at the ends of their ranges: gradients that do not depend on a
-tensor whose values are infinite, NaN or near the largest."""
+"""Block norms at widths between those of the other tests and at the ends of
+their ranges: gradients that do not depend on a tensor whose values are
+infinite, NaN or near the largest."""
 import pytest
 import torch
 
 import quantized_routed_expert_moe_amd as Q
 from tests.expert_util import D, EPS16
-from tests.test_gpu_block_norm import EPS, F, close, dev, formula, make
+from tests.test_gpu_block_norm import EPS, F, close, dev, formula, make, run_both
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,16 @@ def test_gradient_without_a_next_norm_does_not_depend_on_x(H, dtype, post, gate)
             n = H if name == "gate" and gate == "token" else T
             close(d, grads[name], 0.0, (n ** 0.5 * 200 + 8 * n ** 0.5 * min(n, 64) ** 0.5) * F * 8.0 * big, "d" + name)
     assert dx.to(D).isfinite().all()
+
+
+@pytest.mark.parametrize("H", [136, 248, 256])
+@pytest.mark.parametrize("T", [1, 5, 333])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_widths_of_eight_rows_a_workgroup(H, T, gate):
+    run_both(T, H, BF, F32, F32, True, gate, True, 0.5, seed=T)
+
+
+@pytest.mark.parametrize("H,gate", [(136, "channel"), (256, "token")])
+def test_workgroups_that_walk_several_steps(H, gate):
+    """More rows than 512 workgroups of eight take at once, the last step a partial one."""
+    run_both(9003, H, HF, BF, HF, True, gate, True, seed=H)
