@@ -46,6 +46,8 @@ struct StreamArgs {
     int x_rows, y_rows;
     void* y;
     int y_f32;
+    int slots;       // slots that can own a position
+    int unit_shift;  // a workgroup walks up to 2^unit_shift rows of a slot
 };
 
 constexpr int kSegment = 256;  // inputs a wave takes at a time
@@ -158,6 +160,35 @@ __device__ __forceinline__ int stream_slot(const RowMap& m, int i) {
     return -1;
 }
 
+// Of the units of 2^shift rows behind the first of each slot, in slot order, number
+// e: its slot (-1: there are fewer) and first row.  A scan over the slots (S <=
+// 1024) in each wave: a lane counts up to 16 neighbouring slots.
+__device__ __forceinline__ int2 later_unit(const RowMap& m, int e, int shift) {
+    if (!m.offsets) return make_int2((m.R - 1) >> shift > e ? 0 : -1, (e + 1) << shift);
+    const int lane = threadIdx.x & 63, per = (m.S + 63) / 64, s0 = lane * per;
+    int n[16], mine = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) n[j] = j < per && s0 + j < m.S ? max(slot_range(m, s0 + j).y - 1, 0) >> shift : 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) mine += n[j];
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += x;
+    }
+    const uint64_t mask = __ballot(e < sum);
+    if (!mask) return make_int2(-1, 0);
+    int slot = -1, unit = 0, left = e - (sum - mine);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if (slot < 0 && left < n[j]) slot = s0 + j, unit = left + 1;
+        left -= n[j];
+    }
+    const int from = __ffsll((unsigned long long)mask) - 1;
+    return make_int2(__builtin_amdgcn_readlane(slot, from), __builtin_amdgcn_readlane(unit, from) << shift);
+}
+
 // The launch bounds' second number keeps the sums in ordinary registers: the
 // accumulation registers would be read back one by one for the scales.
 // WT 0: 16-bit weights, 1: 4-bit.  SWI: tile 0 holds gate rows, tile 1 the up
@@ -168,9 +199,14 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
     extern __shared__ float red[];  // [waves][NT][MB][64][4]; before that the table of scales
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int col = lane & 15, c = lane >> 4;
-    const int slot = __builtin_amdgcn_readfirstlane(stream_slot(a.rows, blockIdx.y));
+    // The first units of all slots, then the later ones.
+    int2 begin;
+    if ((int)blockIdx.y < a.slots) begin = make_int2(stream_slot(a.rows, blockIdx.y), 0);
+    else begin = later_unit(a.rows, blockIdx.y - a.slots, a.unit_shift);
+    const int slot = __builtin_amdgcn_readfirstlane(begin.x), rb0 = __builtin_amdgcn_readfirstlane(begin.y);
     if (slot < 0) return;
-    const int2 r = slot_range(a.rows, slot);
+    int2 r = slot_range(a.rows, slot);
+    r.y = min(r.y, rb0 + (1 << a.unit_shift));
     const int N = a.N, K = a.K, half = N / 2, width = SWI ? half : N;
     const int n0 = blockIdx.x * (SWI ? 16 : 16 * NT);
     const uint8_t* w = static_cast<const uint8_t*>(a.w) + (size_t)slot * a.w_stride;
@@ -222,7 +258,7 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
             for (int i = 0; i < 4; ++i) to[i] = make_float4(q[2 * i].x, q[2 * i].y, q[2 * i + 1].x, q[2 * i + 1].y);
         }
     };
-    for (int rb = 0; rb < r.y; rb += 16 * MB) {
+    for (int rb = rb0; rb < r.y; rb += 16 * MB) {
         const int nr = min(r.y - rb, 16 * MB);
         f32x4 tot[NT][MB] = {};
         // A pass over the weights.  XR: rows that share one load of x.
@@ -444,10 +480,23 @@ static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     const int mb = mean <= (WT ? 16 : 8) || a.rows.R <= 16 ? 1 : !few || a.rows.R <= 32 || PER == 1 ? 2 : 4;
     const int segs = (a.K + kSegment - 1) / kSegment, turns = (segs + kStreamWaves - 1) / kStreamWaves;
     const int waves = (segs + turns - 1) / turns;
-    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(a, mb, dim3(tiles, slots), waves, s);
     // one tile a workgroup where two would leave CUs without one
-    if (few) return stream_launch_rows<WT, DT, 1, PER, false>(a, mb, dim3(tiles, slots), waves, s);
-    return stream_launch_rows<WT, DT, 2, PER, false>(a, mb, dim3((tiles + 1) / 2, slots), waves, s);
+    const int columns = act || few ? tiles : (tiles + 1) / 2;
+    // Rows that a workgroup walks: one pass where a slot that holds most rows would
+    // be walked longer than all workgroups take, 1280 of them at a time (128 slots of
+    // 1408 x 1408, 1536 rows: 105 us in even slots both ways, 270 and 115 us with half
+    // of them in one; one 4-bit matrix of 1536 x 2048, 16384 rows: 3.7 and 0.79 ms).
+    // Else all of a slot's, as the other workgroups would only look for rows.
+    const int blocks = (a.rows.R + 16 * mb - 1) / (16 * mb);
+    StreamArgs t = a;
+    t.slots = slots;
+    t.unit_shift = mb == 1 ? 4 : mb == 2 ? 5 : 6;
+    const int most = blocks > 3 && blocks > 1 + (long long)columns * slots / 1280 ? 32768 : 1;  // units of a slot
+    while ((a.rows.R - 1) >> t.unit_shift >= most) ++t.unit_shift;
+    const dim3 grid(columns, slots + ((a.rows.R - 1) >> t.unit_shift));
+    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(t, mb, grid, waves, s);
+    if (few) return stream_launch_rows<WT, DT, 1, PER, false>(t, mb, grid, waves, s);
+    return stream_launch_rows<WT, DT, 2, PER, false>(t, mb, grid, waves, s);
 }
 
 template <int DT>
