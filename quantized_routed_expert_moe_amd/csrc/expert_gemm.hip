@@ -15,12 +15,18 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     const int slots = possible_slots(a.rows);
     // Few rows a slot: the weights' stream bounds the call.  Up to how many the
     // streaming kernel is the faster one depends on the tiles that the other
-    // would have.  Few leave CUs idle: one matrix of 2048 x 2048 takes 12.9
-    // streamed and 15.9 us tiled at 64 rows, 19.8 and 15.9 at 96; 8192 x 4096 27
-    // and 40 us at 32 rows, 41 and 41 at 64.  Enough of them read the weights as
-    // fast, and only their start and store count, as much as 12 stages of 64: 256
-    // slots of 1408 x 1408 take 183 and 204 us at 8 rows, 202 and 207 at 12; 128 of
-    // 1536 x 2048 with SwiGLU 156 and 137 us at 2, 188 and 142 at 16.
+    // would have.  Times are us streamed / tiled, bf16.  Few tiles leave CUs idle:
+    //   64 (8192 x 2048, one slot)   16 / 20 at 32 rows, 21 / 20 at 48, 25 / 20 at 64
+    //   128 (8 slots of 2048 x 2048) 18 / 28 at 12, 23 / 29 at 32, 37 / 28 at 48
+    //   256 (16 of 2048 x 2048)      30 / 32 at 2, 31 / 32 at 8, 35 / 32 at 12
+    // Enough of them read the weights as fast, and only their start and store count,
+    // which a long contraction hides (64 slots of 2048 x K, 1024 tiles):
+    //   K = 1024  46 / 50 at 2, 47 / 50 at 8, 52 / 50 at 12
+    //   K = 1536  70 / 78 at 2, 76 / 79 at 8, 83 / 80 at 12
+    //   K = 2048  98 / 91 at 2, 103 / 93 at 8
+    //   K = 4096  228 / 173 at 2
+    // With SwiGLU the steps lie lower: 128 slots of 1536 x 2048 156 / 137 at 2.  One rule
+    // for all leaves up to a quarter at 13 to 32 rows of 128 tiles and at long K.
     const long long tiles = (long long)slots * ((a.N + 127) / 128);
     const int few = tiles <= 64 ? 48 : tiles <= 128 || a.K < 1536 ? 12 : 2;
     if (!a.transpose && a.rows.R <= (long long)few * slots) {

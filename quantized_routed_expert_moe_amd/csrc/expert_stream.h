@@ -62,7 +62,10 @@ constexpr int kTableGroups = 64, kTableStride = kTableGroups + 2;
 constexpr int kFewRows = 4;
 // Waves that split a workgroup's inputs.  Four: more would leave a CU one or
 // two workgroups (128 4-bit experts of 4096 x 7168 take 353 us at 1.5 rows a
-// slot and 1044 us at 30, with eight 420 and 1229 us).
+// slot and 1044 us at 30, with eight 420 and 1229 us).  With few workgroups, by
+// four and by eight: one bf16 matrix of 2048 x 2048 5.0 and 5.0 us (128
+// workgroups), one 4-bit matrix of 4096 x 2048 4.2 and 4.2, of 4096 x 4096 6.4 and
+// 5.7 (256), 16 4-bit gate/up of 1536 x 2048 8.7 and 10.8 (768).
 constexpr int kStreamWaves = 4;
 
 template <int DT>
