@@ -395,20 +395,28 @@ __device__ __forceinline__ void tile_short(const TileArgs& a, int q0, int c0, in
 }
 
 // Weight gradient of a slot (or part) without rows: tile `tile` of `tiles` writes
-// its share of the matrix's zeros, each wave one run of them.  128 slots of 1408 x
-// 2048 with 8 rows in all (small tiles), fp32 and bf16: 224 and 114 us, 6.6 and 6.5
-// TB/s; a workgroup's runs in turn 249 and 112 us, the tiles' own rows 230 and 120.
-// Odd widths gain most: 128 of 2064 x 472, bf16, 39 us, by the tiles' rows 87 us.
+// its share of the matrix's zeros.  A gradient that the last-level cache holds
+// goes through it, a workgroup's runs of 16 bytes a thread in turn; a larger one
+// past it, each wave in one run.  Slots without any row, us through and past: 45 of
+// 1000 x 1400, fp32 (252 MB) 32 and 43; 12 of 2816 x 2048 (277 MB) 35 and 44, 45 (1.04
+// GB) 169 and 158; 128 of 1408 x 2048 with 64 rows in all (1.5 GB) 253 and 225.  By the
+// tiles' own rows odd widths cost twice as much (128 of 2064 x 472, bf16: 87 us, 39
+// in runs).
 template <typename C>
 __device__ __forceinline__ void tile_zero(const TileArgs& a, int slot, int tile, int tiles) {
     const size_t units = (size_t)a.N * a.K / (a.y_f32 ? 4 : 8);  // of 16 bytes
     const size_t share = ((units + tiles - 1) / tiles + 63) & ~(size_t)63;
-    const size_t from = min(units, tile * share), end = min(units, from + share), run = (end - from) / (C::W * 64) * 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const size_t to = wave == C::W - 1 ? end : from + (wave + 1) * run;
+    const size_t from = min(units, tile * share), end = min(units, from + share);
     u32x4* y = static_cast<u32x4*>(a.y) + slot * units;
     const u32x4 zero = {0, 0, 0, 0};
-    for (size_t i = from + wave * run + lane; i < to; i += 64) __builtin_nontemporal_store(zero, y + i);
+    if (a.splits > 1 || a.rows.S * units <= (300u << 20) / 16) {
+        for (size_t i = from + threadIdx.x; i < end; i += C::THREADS) y[i] = zero;
+    } else {
+        const size_t run = (end - from) / (C::W * 64) * 64;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const size_t to = wave == C::W - 1 ? end : from + (wave + 1) * run;
+        for (size_t i = from + wave * run + lane; i < to; i += 64) __builtin_nontemporal_store(zero, y + i);
+    }
 }
 
 // The tile's rows, rounded and stored: a block of 32 rows at a time through
