@@ -554,7 +554,9 @@ moe_status moe_expert_gemv_w4(const void* x, int dtype, const void* q, const voi
  *            MOE_GATE_TOKEN: [T], MOE_GATE_NONE: gate is NULL.
  * H          a multiple of 8, 8..MOE_MAX_NORM_WIDTH.  T in 0..2^24.
  * eps        >= 0, finite; res_scale finite.
- * h is computed from the unrounded x_out; each output is rounded once.
+ * h is computed from the unrounded x_out; each output is rounded once.  Squares
+ * are summed in fp32: rows whose sum of squares passes its range (values of about
+ * 1e19) come out as 0 or NaN.
  *
  * moe_block_norm_backward: the gradients of the same expressions for given
  * dx_out and dh.  The row statistics are recomputed from x and y.
