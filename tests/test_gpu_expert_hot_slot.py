@@ -75,3 +75,45 @@ def test_more_blocks_of_rows_than_workgroups(group):
     y.fill_(7.0)
     Q.moe_expert_gemv_w4(x, q, sc, z, group, off, y)
     assert torch.equal(y[5:], want[at[5:]])
+
+
+def test_captured_calls_follow_the_offsets():
+    """One graph of a product, a 4-bit product and a weight gradient, replayed over batches that are even, in one slot,
+    nearly empty and empty: each replay equals the eager calls."""
+    S, N, K, group, P = 24, 72, 256, 64, 400
+    g = torch.Generator().manual_seed(6)
+    x, dy = (torch.randn((P, n), generator=g).to(BF).cuda() for n in (K, N))
+    w = torch.randn((S, N, K), generator=g).to(BF).cuda()
+    q, sc, z = (t.cuda() for t in w4.weights(S, N, K, group, BF, True, 7))
+    off, out = torch.zeros(S + 1, dtype=torch.int32, device="cuda"), {}
+    out["y"], out["y4"] = (torch.zeros((P, N), device="cuda") for _ in range(2))
+    out["dw"] = torch.zeros((S, N, K), dtype=BF, device="cuda")
+    ws = torch.empty(max(1, Q.moe_expert_gemm_wgrad_workspace_size(S, N, K, P)), dtype=torch.uint8, device="cuda")
+
+    def calls():
+        Q.moe_expert_gemm(x, w, off, out["y"])
+        Q.moe_expert_gemv_w4(x, q, sc, z, group, off, out["y4"])
+        Q.moe_expert_gemm_wgrad(dy, x, off, out["dw"], ws=ws)
+
+    sizes = [[16] * 24 + [0], [0] * 11 + [400] + [0] * 12, [0] * 5 + [2] + [0] * 18, [0] * 24, skewed(24, {3: 250}, 100, 8)]
+    starts = [torch.tensor([0] + s[:24]).cumsum(0).to(torch.int32) for s in sizes]
+    want = []
+    for o in starts:
+        off.copy_(o)
+        for v in out.values():
+            v.fill_(7.0)
+        calls()
+        want.append([v.clone() for v in out.values()])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        calls()
+    for _ in range(2):
+        for o, expected in zip(starts, want):
+            off.copy_(o)
+            for v in out.values():
+                v.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(v, e) for v, e in zip(out.values(), expected))
+            (out["y"] * 2).sum()  # eager work of the program between replays
