@@ -32,6 +32,14 @@
  *   moe_block_norm(_backward) norm, gate, residual sum and next norm in one
  *                             pass, and their gradients
  *   moe_swiglu(_backward)     the activation between two products
+ *   moe_expert_gemm_bias /    the forward product with bias, activation and
+ *   moe_expert_act_backward   residual in its epilogue, and the gradients of
+ *                             the activation and the biases
+ *   moe_balance_loss /        the router's losses and per-expert counts, and
+ *   moe_route_backward        the gate logits' gradient
+ *   moe_combine_backward      the combine's gradients: pairs and weights
+ *   moe_grad_norm /           the norm over a list of gradients, and their
+ *   moe_grad_clip             clipping
  *
  * Conventions for every call:
  *   - Pointers marked "device" are device (HBM) addresses, "host" are host
@@ -70,7 +78,7 @@ typedef enum moe_status {
 } moe_status;
 
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
-/* MOE_F16 is taken by the expert products, block norms and SwiGLU only. */
+/* MOE_F16 is taken by the calls for unquantized experts, block norms, activations and training only. */
 typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 typedef enum moe_path { MOE_PATH_AUTO = 0, MOE_PATH_DECODE = 1, MOE_PATH_PREFILL = 2, MOE_PATH_PREFILL_I8 = 3 } moe_path;
 typedef enum moe_format {
@@ -84,7 +92,16 @@ typedef enum moe_format {
 
 /* How a call's rows are addressed from batch position q. */
 typedef enum moe_rows { MOE_ROWS_POSITION = 0, MOE_ROWS_PAIR = 1, MOE_ROWS_TOKEN = 2 } moe_rows;
-typedef enum moe_act { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+/* MOE_ACT_SILU and the ones behind it are taken by moe_expert_gemm_bias and moe_expert_act_backward only. */
+typedef enum moe_act {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SWIGLU = 1,
+    MOE_ACT_SILU = 2,      /* v / (1 + e^-v) */
+    MOE_ACT_GELU = 3,      /* v (1 + erf(v / sqrt 2)) / 2 */
+    MOE_ACT_GELU_TANH = 4, /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    MOE_ACT_RELU = 5       /* max(v, 0) */
+} moe_act;
+typedef enum moe_norm_kind { MOE_NORM_L2 = 0, MOE_NORM_MAX = 1 } moe_norm_kind;
 typedef enum moe_gate { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate;
 
 /* Limits checked by the calls below. */
@@ -600,6 +617,148 @@ moe_status moe_swiglu(const void* gu, int dtype, int R, int I, const int32_t* sl
                       void* stream);
 moe_status moe_swiglu_backward(const void* gu, const void* dh, int dtype, int R, int I, const int32_t* slot_offsets,
                                int S, void* dgu, void* h, void* stream);
+
+/* ------------------------------- products with bias, activation, residual
+ * moe_expert_gemm (transpose 0) with an epilogue, for experts and projections
+ * that carry biases and for training:
+ *   z[iy(q), n] = sum over j < K of x[ix(q), j] * w_s[n, j] + bias_s[n]
+ *   y[iy(q), n] = act(z[iy(q), n]) + residual[iy(q), n]
+ * act = MOE_ACT_SWIGLU: n < N / 2 and act = silu(z[n]) * z[N / 2 + n].
+ *
+ * bias       device, [S, N], bias_dtype: dtype or MOE_F32; or NULL.
+ * residual   device, res_dtype: dtype or MOE_F32, rows and width of y; or NULL.
+ *            May be y itself where the types agree (y += ...).
+ * act        any MOE_ACT_*.
+ * z          device, [R, N], dtype: z rounded once, for moe_expert_act_backward,
+ *            its rows addressed as y's; or NULL.  z, y and residual do not
+ *            overlap otherwise.
+ * The other arguments as for moe_expert_gemm (y_dtype: dtype or MOE_F32).  act and
+ * the sum take z in fp32, y is rounded once.  Rows of positions that no slot owns
+ * are left as they were, in y and in z.  All pointers are 16-byte aligned.
+ *
+ * moe_expert_act_backward: for given dy, the gradients of z and of the biases,
+ *   dz[i(q), n] = dy[i(q), n] * act'(z[i(q), n])
+ *   dbias_s[n]  = sum over q of slot s of dz[i(q), n]   (dz in fp32)
+ * for the products' gradients, which take dz (moe_expert_gemm with transpose 1,
+ * moe_expert_gemm_wgrad).  The residual's gradient is dy itself.
+ * dy         device, rows of N (SWIGLU: N / 2), dtype (any of the three).
+ * z, dz      device, rows of N, dtype.  Both NULL for MOE_ACT_NONE (dz is dy).  dz may
+ *            be z itself, and dy itself where the widths agree (in place).
+ * h          device, rows of dy's width, dtype, or NULL: act(z) once more, for the next
+ *            product's weight gradient.  NULL for MOE_ACT_NONE.  May be dy itself.
+ * rows       how all of them are addressed: MOE_ROWS_POSITION or MOE_ROWS_PAIR.
+ * dbias      device, fp32 [S, N], every element written (zeros for a slot that owns no
+ *            position), or NULL.  Given for MOE_ACT_NONE.
+ * slot_offsets, S, R, perm_pair, N  as for moe_expert_gemm (N a multiple of 8, SWIGLU
+ *            of 16, N <= 2^20).
+ * ws         device workspace of moe_expert_act_backward_workspace_size (0 for
+ *            arguments out of range), 16-byte aligned; unused without dbias.
+ * Sums over rows are taken in an order fixed by the sizes and offsets.
+ */
+moe_status moe_expert_gemm_bias(const void* x, int dtype, const void* w, size_t w_stride, int S, int N, int K,
+                                const void* bias, int bias_dtype, const void* residual, int res_dtype,
+                                const int32_t* slot_offsets, int R, const int32_t* perm_pair, int k, int x_rows,
+                                int y_rows, int act, void* y, int y_dtype, void* z, void* stream);
+size_t moe_expert_act_backward_workspace_size(int S, int N, int R);
+moe_status moe_expert_act_backward(const void* dy, const void* z, int dtype, int S, int N,
+                                   const int32_t* slot_offsets, int R, const int32_t* perm_pair, int rows, int act,
+                                   void* dz, void* h, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------ router's losses and gradients
+ * The balance loss, the z loss and the experts' counts of a batch of G
+ * sequences (segments): sequence g owns the rows t in [seq_offsets[g],
+ * seq_offsets[g + 1]), n_g of them, n of all; rows outside belong to none
+ * (padding).  With p_t = softmax(logits_t) (MOE_SCORE_SOFTMAX) or
+ * s_t / sum(s_t), s = 1 / (1 + e^-logit) (MOE_SCORE_SIGMOID):
+ *   counts[g, e] = pairs (t, j) of sequence g with topk_ids[t, j] = e
+ *   probs[g, e]  = mean of p[t, e] over the rows of sequence g
+ *   losses[0]    = E / (k n) * sum over g and e of counts[g, e] * probs[g, e]
+ *   losses[1]    = mean over the n rows of (log sum over e of e^logits[t, e])^2
+ * With sequences of one length losses[0] is the mean of their balance losses
+ * sum_e f_e P_e with f_e = E counts_e / (k n_g); it is 1 where all is even.
+ *
+ * logits     device, fp32 [T, E].  A logit of -inf has probability 0; a row of
+ *            nothing else has all probabilities 0 and adds nothing to losses[1].
+ * topk_ids   device, int32 [T, k]; ids outside [0, E) are not counted.
+ * T, E, k    as for moe_route_topk; T up to 2^24 / k.
+ * seq_offsets  device, int32 [G + 1], not decreasing; NULL with G = 1: one
+ *            sequence of all T rows.  G in 1..MOE_MAX_SEQUENCES.
+ * counts     device, int32 [G, E].  probs  device, fp32 [G, E].  losses  device, fp32
+ *            [2].  All of them are written: zeros for a sequence without rows, and
+ *            losses of 0 for n = 0.
+ * ws         device workspace of moe_balance_loss_workspace_size (0 for arguments
+ *            out of range), 16-byte aligned.
+ * Sums are fp32 in an order fixed by the sizes and offsets.
+ *
+ * moe_route_backward: the gradient of the logits,
+ *   dlogits = (gradient through topk_w) + dlosses[0] * d losses[0] / d logits
+ *                                       + dlosses[1] * d losses[1] / d logits
+ * with topk_w = moe_route_topk's weights of the given ids (which are constants, as
+ * are the counts), recomputed from the logits.
+ * dtopk_w    device, fp32 [T, k], or NULL: no gradient through the weights.
+ * score, renormalize, scale  as for moe_route_topk.
+ * counts, dlosses  device, int32 [G, E] and fp32 [2]; both NULL: no losses, and
+ *            seq_offsets is not read.  counts may hold another batch's or all
+ *            ranks' sums.
+ * dlogits    device, [T, E], out_dtype MOE_F32, MOE_BF16 or MOE_F16 (one rounding), all
+ *            rows written; may be logits itself (MOE_F32).
+ * A pair whose id lies outside [0, E) has no weight: its dtopk_w is not used.
+ */
+#define MOE_MAX_SEQUENCES 1024
+size_t moe_balance_loss_workspace_size(int T, int E, int G);
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, int T, int E, int k, int score,
+                            const int32_t* seq_offsets, int G, int32_t* counts, float* probs, float* losses, void* ws,
+                            size_t ws_bytes, void* stream);
+moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, const float* dtopk_w, int T, int E, int k,
+                              int score, int renormalize, float scale, const int32_t* counts, const float* dlosses,
+                              const int32_t* seq_offsets, int G, void* dlogits, int out_dtype, void* stream);
+
+/* ------------------------------------------------------ combine's gradient
+ * The gradients of moe_combine for given dy (the shared expert's is dy itself).
+ * For a resident pair p = t*k + j (moe_combine's rule):
+ *   dy_pairs[p] = topk_w[p] * dy[t]        dtopk_w[p] = sum over h of y_pairs[p, h] * dy[t, h]
+ * and zeros for the others, whose rows of y_pairs are not used.
+ * dy         device, [T, H], dy_dtype (any of the three).
+ * y_pairs, dy_pairs  device, [T*k, H], pairs_dtype (any of the three).  dy_pairs may be
+ *            y_pairs itself (in place).
+ * dtopk_w    device, fp32 [T, k].
+ * H % 8 == 0, T*k up to 2^24.  Sums are fp32 in a fixed order.  dy, y_pairs and dy_pairs are
+ * 16-byte aligned.
+ */
+moe_status moe_combine_backward(const void* dy, int dy_dtype, const void* y_pairs, int pairs_dtype,
+                                const int32_t* topk_ids, const float* topk_w, const int32_t* slot_of_expert, int E,
+                                int S, int T, int k, int H, void* dy_pairs, float* dtopk_w, void* stream);
+
+/* -------------------------------------------------- gradient norm, clipping
+ * One norm over a list of n gradients, and their scaling to a largest norm:
+ *   total = |scale| * sqrt(sum of squares)   (MOE_NORM_L2)
+ *         = |scale| * largest magnitude      (MOE_NORM_MAX; NaN if any is)
+ *   outs[i] = grads[i] * scale * min(1, max_norm / (total + eps))
+ * scale undoes a loss scale.  A total of infinity gives a factor of 0, one of
+ * NaN a factor of NaN.
+ *
+ * grads, counts, dtypes  host arrays of n: device addresses (aligned to their
+ *            elements, any more is not needed), elements (0..2^40; NULL may stand for 0),
+ *            types (any of the three).  Read during the call only; a captured call
+ *            keeps the addresses.
+ * outs, out_dtypes  the same for what is written; an out is its gradient itself
+ *            (in place, one type) or does not overlap any gradient.  outs = NULL:
+ *            all in place.  In place a factor of 1 leaves the memory as it is.
+ * No two gradients overlap.  n in 0..2^20.
+ * total      device, fp32 [1].  moe_grad_clip reads it: between the two calls the
+ *            caller may join it with other ranks' norms.
+ * max_norm   >= 0; eps >= 0, finite; scale finite.
+ * ws         device workspace of moe_grad_norm_workspace_size(n), 16-byte aligned.
+ * Squares are summed in 64 bits in an order fixed by the counts, so that no sum
+ * overflows; the factor is taken in 64 bits and rounded to fp32, and each output
+ * once more.
+ */
+size_t moe_grad_norm_workspace_size(int n);
+moe_status moe_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n, int kind,
+                         float scale, float* total, void* ws, size_t ws_bytes, void* stream);
+moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, void* const* outs,
+                         const int32_t* out_dtypes, int n, const float* total, float max_norm, float eps, float scale,
+                         void* stream);
 
 /* ------------------------------------------------------------ stage timers
  * Diagnostics: one hipEvent pair per launch of a stage, attached to the

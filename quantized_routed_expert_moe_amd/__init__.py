@@ -99,6 +99,20 @@ def lib() -> ctypes.CDLL:
             [sz, vp]
         L.moe_swiglu.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp]
         L.moe_swiglu_backward.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, vp, vp]
+        L.moe_expert_gemm_bias.argtypes = [vp, i32, vp, sz, i32, i32, i32, vp, i32, vp, i32, vp, i32, vp] + [i32] * 4 + \
+            [vp, i32, vp, vp]
+        L.moe_expert_act_backward_workspace_size.argtypes = [i32] * 3
+        L.moe_expert_act_backward_workspace_size.restype = sz
+        L.moe_expert_act_backward.argtypes = [vp, vp, i32, i32, i32, vp, i32, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_loss_workspace_size.argtypes = [i32] * 3
+        L.moe_balance_loss_workspace_size.restype = sz
+        L.moe_balance_loss.argtypes = [vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_route_backward.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, i32, vp, i32, vp]
+        L.moe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+        L.moe_grad_norm_workspace_size.argtypes = [i32]
+        L.moe_grad_norm_workspace_size.restype = sz
+        L.moe_grad_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [vp, vp, vp, vp, vp, i32, vp, f32, f32, f32, vp]
         for name in ("moe_route_topk", "moe_build_expert_batches", "moe_route_and_batch", "moe_count_routes",
                      "moe_pack_expert", "moe_unpack_expert", "moe_pack_q4k", "moe_pack_q8_0",
                      "moe_validate_slot_map", "moe_expert_ffn_q4k", "moe_expert_ffn_q8_0", "moe_expert_ffn_mxfp4",
@@ -106,7 +120,9 @@ def lib() -> ctypes.CDLL:
                      "moe_combine", "moe_layer_decode",
                      "moe_timer_begin", "moe_timer_end", "moe_timer_read", "moe_hbm_read_probe",
                      "moe_prefill_inner_probe", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemv_w4",
-                     "moe_block_norm", "moe_block_norm_backward", "moe_swiglu", "moe_swiglu_backward"):
+                     "moe_block_norm", "moe_block_norm_backward", "moe_swiglu", "moe_swiglu_backward",
+                     "moe_expert_gemm_bias", "moe_expert_act_backward", "moe_balance_loss", "moe_route_backward",
+                     "moe_combine_backward", "moe_grad_norm", "moe_grad_clip"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -438,7 +454,7 @@ def moe_layer_decode(fmt: int, logits, x, k: int, score: int, renormalize: bool,
 
 MOE_F16 = 2
 MOE_ROWS_POSITION, MOE_ROWS_PAIR, MOE_ROWS_TOKEN = 0, 1, 2
-MOE_ACT_NONE, MOE_ACT_SWIGLU = 0, 1
+MOE_ACT_NONE, MOE_ACT_SWIGLU, MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU = range(6)
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN = 0, 1, 2
 
 _torch = None
@@ -691,6 +707,254 @@ def moe_swiglu_backward(gu, dh, dgu, h=None, slot_offsets=None, stream=None):
     _norm_like(dgu, gu.shape, gu.dtype, "dgu")
     gp, dp, op, up, hp = _op_ptrs(dev, "gu dh slot_offsets dgu h", gu, dh, slot_offsets, dgu, h)
     _check(lib().moe_swiglu_backward(gp, dp, _op_code(gu, "gu"), R, I, op, S, up, hp, _op_stream(dev, stream)))
+
+
+# ------------------------- products with bias, activation and residual
+# As above: shapes give the sizes, every tensor lives on the current device, and no
+# call records itself for autograd.
+
+def moe_expert_gemm_bias(x, w, bias, residual, slot_offsets, y, perm_pair=None, k: int = 1,
+                         x_rows: int = MOE_ROWS_POSITION, y_rows: int = MOE_ROWS_POSITION, act: int = MOE_ACT_NONE,
+                         z=None, stream=None):
+    """y rows = act(x rows times their slot's matrix of w [S, N, K] + bias [S, N]) + residual rows; z rows = the sums
+    before act.  bias, residual and z may be None; residual may be y."""
+    dev = _op_device()
+    shape, strides = w.shape, w.stride()
+    if len(shape) != 3 or strides[2] != 1 or (strides[1] != shape[2] and shape[1] != 1):
+        raise ValueError("w must be [S, N, K] with contiguous matrices")
+    S, N, K = shape
+    R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
+    width = N // 2 if act == MOE_ACT_SWIGLU else N
+    _op_matrix(x, K, R, x_rows, k, "x")
+    _op_matrix(y, width, R, y_rows, k, "y")
+    if w.dtype != x.dtype:
+        raise TypeError(f"w has dtype {w.dtype}, x {x.dtype}")
+    if bias is not None and bias.shape != (S, N):
+        raise ValueError(f"bias has shape {tuple(bias.shape)}, expected [{S}, {N}]")
+    if residual is not None:
+        _op_matrix(residual, width, R, y_rows, k, "residual")
+    if z is not None:
+        _op_matrix(z, N, R, y_rows, k, "z")
+        if z.dtype != x.dtype:
+            raise TypeError(f"z has dtype {z.dtype}, x {x.dtype}")
+    xp, bp, rp, op, pp, yp, zp = _op_ptrs(dev, "x bias residual slot_offsets perm_pair y z", x, bias, residual,
+                                          slot_offsets, perm_pair, y, z)
+    if w.get_device() != dev or (w.requires_grad and _torch.is_grad_enabled()):
+        _op_refuse(dev, "w", w)
+    _check(lib().moe_expert_gemm_bias(
+        xp, _op_code(x, "x"), w.data_ptr(), 2 * (strides[0] if S > 1 else N * K), S, N, K, bp,
+        MOE_F32 if bias is None else _op_code(bias, "bias"), rp,
+        MOE_F32 if residual is None else _op_code(residual, "residual"), op, R, pp, k, x_rows, y_rows, act, yp,
+        _op_code(y, "y"), zp, _op_stream(dev, stream)))
+
+
+def moe_expert_act_backward_workspace_size(S: int, N: int, R: int) -> int:
+    return int(lib().moe_expert_act_backward_workspace_size(S, N, R))
+
+
+def moe_expert_act_backward(dy, z, slot_offsets, dz, dbias, perm_pair=None, rows: int = MOE_ROWS_POSITION,
+                            act: int = MOE_ACT_NONE, h=None, ws=None, stream=None):
+    """dz = dy act'(z) rows and dbias [S, N] = their sums over each slot; h = act(z) again unless None.  With
+    MOE_ACT_NONE z, dz and h are None and dbias sums dy; else dbias may be None."""
+    dev = _op_device()
+    dtype, swiglu = dy.dtype, act == MOE_ACT_SWIGLU
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    N = dy.shape[1] * (2 if swiglu else 1)
+    S = dbias.shape[0] if dbias is not None and dbias.dim() == 2 else 1 if slot_offsets is None else slot_offsets.shape[0] - 1
+    R = _op_rows(slot_offsets, S, perm_pair, dy, (rows,), 1)
+    if rows not in (MOE_ROWS_POSITION, MOE_ROWS_PAIR):
+        raise ValueError(f"rows = {rows} is neither MOE_ROWS_POSITION nor MOE_ROWS_PAIR")
+    for name, t, cols in (("dy", dy, dy.shape[1]), ("z", z, N), ("dz", dz, N), ("h", h, dy.shape[1])):
+        if t is not None:
+            _op_matrix(t, cols, R, rows, 1, name)
+            if t.dtype != dtype:
+                raise TypeError(f"{name} has dtype {t.dtype}, dy {dtype}")
+    if dbias is not None and (dbias.dtype != _F32 or dbias.shape != (S, N)):
+        raise ValueError(f"dbias must be float32 [{S}, {N}]")
+    dp, zp, op, pp, gp, hp, bp, sp = _op_ptrs(dev, "dy z slot_offsets perm_pair dz h dbias ws", dy, z, slot_offsets,
+                                              perm_pair, dz, h, dbias, ws)
+    _check(lib().moe_expert_act_backward(dp, zp, _op_code(dy, "dy"), S, N, op, R, pp, rows, act, gp, hp, bp, sp,
+                                         0 if ws is None else ws.numel() * ws.element_size(), _op_stream(dev, stream)))
+
+
+# --------------------------------------- router's losses and gradients
+
+def _router_shapes(logits, topk_ids, seq_offsets) -> tuple:
+    if logits.dim() != 2 or logits.dtype != _F32:
+        raise ValueError("logits must be float32 [T, E]")
+    T, E = logits.shape
+    if topk_ids.dim() != 2 or topk_ids.dtype != _I32 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must be int32 [{T}, k]")
+    G = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.dtype != _I32 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets must be int32 [G + 1]")
+        G = seq_offsets.shape[0] - 1
+    return T, E, topk_ids.shape[1], G
+
+
+def moe_balance_loss_workspace_size(T: int, E: int, G: int = 1) -> int:
+    return int(lib().moe_balance_loss_workspace_size(T, E, G))
+
+
+def moe_balance_loss(logits, topk_ids, score: int, counts, probs, losses, seq_offsets=None, ws=None, stream=None):
+    """losses [2] = (balance loss, z loss) of a routed batch, with counts (int32) and mean probabilities (fp32) [G, E]
+    of its G sequences; seq_offsets [G + 1] None: one sequence of all rows."""
+    dev = _op_device()
+    T, E, k, G = _router_shapes(logits, topk_ids, seq_offsets)
+    if counts.dtype != _I32 or counts.shape != (G, E) or probs.dtype != _F32 or probs.shape != (G, E):
+        raise ValueError(f"counts and probs must be int32 and float32 [{G}, {E}]")
+    if losses.dtype != _F32 or losses.shape != (2,):
+        raise ValueError("losses must be float32 [2]")
+    lp, ip, cp, pp, op, sp, wp = _op_ptrs(dev, "logits topk_ids counts probs losses seq_offsets ws", logits, topk_ids,
+                                          counts, probs, losses, seq_offsets, ws)
+    _check(lib().moe_balance_loss(lp, ip, T, E, k, score, sp, G, cp, pp, op, wp,
+                                  0 if ws is None else ws.numel() * ws.element_size(), _op_stream(dev, stream)))
+
+
+def moe_route_backward(logits, topk_ids, dtopk_w, score: int, renormalize: bool, scale: float, counts, dlosses,
+                       seq_offsets, dlogits, stream=None):
+    """dlogits [T, E] (fp32, bf16 or fp16) for the gradients of moe_route_topk's weights (dtopk_w [T, k] or None) and of
+    moe_balance_loss's losses (dlosses [2] with the counts, or both None)."""
+    dev = _op_device()
+    T, E, k, G = _router_shapes(logits, topk_ids, seq_offsets)
+    if dtopk_w is not None and (dtopk_w.dtype != _F32 or dtopk_w.shape != (T, k)):
+        raise ValueError(f"dtopk_w must be float32 [{T}, {k}]")
+    if (counts is None) != (dlosses is None):
+        raise ValueError("counts and dlosses go together")
+    if counts is not None and (counts.dtype != _I32 or counts.shape != (G, E)):
+        raise ValueError(f"counts must be int32 [{G}, {E}]")
+    if dlosses is not None and (dlosses.dtype != _F32 or dlosses.shape != (2,)):
+        raise ValueError("dlosses must be float32 [2]")
+    if dlogits.shape != (T, E):
+        raise ValueError(f"dlogits must be [{T}, {E}]")
+    lp, ip, wp, cp, gp, sp, dp = _op_ptrs(dev, "logits topk_ids dtopk_w counts dlosses seq_offsets dlogits", logits,
+                                          topk_ids, dtopk_w, counts, dlosses, seq_offsets, dlogits)
+    _check(lib().moe_route_backward(lp, ip, wp, T, E, k, score, int(bool(renormalize)), float(scale), cp, gp, sp, G, dp,
+                                    _op_code(dlogits, "dlogits"), _op_stream(dev, stream)))
+
+
+def moe_combine_backward(dy, y_pairs, topk_ids, topk_w, slot_of_expert, S: int, dy_pairs, dtopk_w, stream=None):
+    """dy_pairs [T*k, H] and dtopk_w [T, k] of moe_combine for given dy [T, H]; zeros for pairs that are not resident."""
+    dev = _op_device()
+    if topk_ids.dim() != 2 or topk_ids.dtype != _I32:
+        raise ValueError("topk_ids must be int32 [T, k]")
+    T, k = topk_ids.shape
+    if dy.dim() != 2 or dy.shape[0] != T:
+        raise ValueError(f"dy must be [{T}, H]")
+    H = dy.shape[1]
+    for name, t in (("topk_w", topk_w), ("dtopk_w", dtopk_w)):
+        if t.dtype != _F32 or t.shape != (T, k):
+            raise ValueError(f"{name} must be float32 [{T}, {k}]")
+    if y_pairs.shape != (T * k, H):
+        raise ValueError(f"y_pairs must be [{T * k}, {H}]")
+    _norm_like(dy_pairs, y_pairs.shape, y_pairs.dtype, "dy_pairs")
+    if slot_of_expert.dim() != 1 or slot_of_expert.dtype != _I32:
+        raise ValueError("slot_of_expert must be int32 [E]")
+    dp, yp, ip, wp, mp, op, gp = _op_ptrs(dev, "dy y_pairs topk_ids topk_w slot_of_expert dy_pairs dtopk_w", dy, y_pairs,
+                                          topk_ids, topk_w, slot_of_expert, dy_pairs, dtopk_w)
+    _check(lib().moe_combine_backward(dp, _op_code(dy, "dy"), yp, _op_code(y_pairs, "y_pairs"), ip, wp, mp,
+                                      slot_of_expert.shape[0], S, T, k, H, op, gp, _op_stream(dev, stream)))
+
+
+# ------------------------------------------- gradient norm and clipping
+
+class moe_tensor_list:
+    """Tensors as the list calls take them: checked once, their storages kept alive.  A program whose gradients stay
+    where they are builds it once; the calls also take a plain list and build it each time."""
+
+    def __init__(self, tensors):
+        self.device = _op_device()
+        grad = _torch.is_grad_enabled()
+        tensors = list(tensors)
+        n = len(tensors)
+        for i, t in enumerate(tensors):
+            if not isinstance(t, _Tensor) or t.get_device() != self.device or not t.is_contiguous() or \
+                    (grad and t.requires_grad):
+                _op_refuse(self.device, f"tensor {i}", t)
+        codes = [_op_code(t, "a tensor") for t in tensors]
+        counts = [t.numel() for t in tensors]
+        self.tensors = [t.detach() for t in tensors]
+        at = [t.data_ptr() for t in tensors]
+        self.ranges = sorted((a, a + c * (4 if code == MOE_F32 else 2)) for a, c, code in zip(at, counts, codes) if c)
+        for (_, end), (start, _) in zip(self.ranges, self.ranges[1:]):
+            if start < end:
+                raise ValueError("two tensors of the list overlap")
+        self.n, self.total, self.counts, self.codes, self.at = n, sum(counts), counts, codes, at
+        self.c_at, self.c_counts, self.c_codes = (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*counts), \
+            (ctypes.c_int32 * n)(*codes)
+
+    def __len__(self) -> int:
+        return self.n
+
+
+def _op_list(tensors, device: int) -> moe_tensor_list:
+    lst = tensors if isinstance(tensors, moe_tensor_list) else moe_tensor_list(tensors)
+    if lst.device != device:
+        raise TypeError(f"the list's tensors must be on the current device (cuda:{device})")
+    return lst
+
+
+def _op_total(total) -> None:
+    if total.dtype != _F32 or total.numel() != 1:
+        raise ValueError("total must be one float32")
+
+
+def moe_grad_norm_workspace_size(n: int) -> int:
+    return int(lib().moe_grad_norm_workspace_size(n))
+
+
+MOE_NORM_L2, MOE_NORM_MAX = 0, 1
+
+
+def moe_grad_norm(grads, total, kind: int = MOE_NORM_L2, scale: float = 1.0, ws=None, stream=None):
+    """total [1] = |scale| times the norm over all of grads (a list of tensors or a moe_tensor_list)."""
+    dev = _op_device()
+    lst = _op_list(grads, dev)
+    _op_total(total)
+    tp, sp = _op_ptrs(dev, "total ws", total, ws)
+    _check(lib().moe_grad_norm(lst.c_at, lst.c_counts, lst.c_codes, lst.n, kind, float(scale), tp, sp,
+                               0 if ws is None else ws.numel() * ws.element_size(), _op_stream(dev, stream)))
+
+
+def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float = 1.0, outs=None, stream=None):
+    """grads times scale min(1, max_norm / (total + eps)), in place or into outs (the same shapes, any of the types)."""
+    dev = _op_device()
+    lst = _op_list(grads, dev)
+    _op_total(total)
+    tp, = _op_ptrs(dev, "total", total)
+    op = oc = None
+    if outs is not None:
+        out = _op_list(outs, dev)
+        if out.counts != lst.counts:
+            raise ValueError("outs must have the sizes of grads")
+        _op_apart(lst, out)
+        op, oc = out.c_at, out.c_codes
+    _check(lib().moe_grad_clip(lst.c_at, lst.c_counts, lst.c_codes, op, oc, lst.n, tp, float(max_norm), float(eps),
+                               float(scale), _op_stream(dev, stream)))
+
+
+def _op_apart(lst: moe_tensor_list, out: moe_tensor_list) -> None:
+    """Every output is its own gradient or overlaps none."""
+    if out is lst or out.at == lst.at:
+        if out.codes != lst.codes:
+            raise ValueError("an output is its gradient in another type")
+        return
+    own = {a: code for a, c, code in zip(lst.at, lst.counts, lst.codes) if c}
+    for i, (a, c) in enumerate(zip(out.at, out.counts)):
+        if c and a == lst.at[i]:
+            if out.codes[i] != own[a]:
+                raise ValueError("an output is its gradient in another type")
+    starts = [r[0] for r in lst.ranges]
+    import bisect
+    for i, (a, c, code) in enumerate(zip(out.at, out.counts, out.codes)):
+        if not c or a == lst.at[i]:
+            continue
+        end = a + c * (4 if code == MOE_F32 else 2)
+        j = bisect.bisect_left(starts, end)
+        if j and lst.ranges[j - 1][1] > a:
+            raise ValueError("an output overlaps another gradient")
 
 
 # ------------------------------------------------------------ host leg

@@ -22,7 +22,9 @@ SOURCES = ["abi.cpp", "route.hip", "batches.hip", "route_batches.hip", "ffn_deco
            "combine.hip", "layer_decode.hip", "hbm_probe.hip", "prefill_probe.hip", "ffn_prefill_i8.hip",
            "abi_ops.cpp", "expert_gemm.hip", "expert_w4.hip", "expert_stream_bf16.hip",
            "expert_stream_f16.hip", "expert_tile_bf16.hip", "expert_tile_f16.hip", "block_norm.hip", "block_norm_f32.hip",
-           "block_norm_bf16.hip", "block_norm_f16.hip", "swiglu.hip"]
+           "block_norm_bf16.hip", "block_norm_f16.hip", "swiglu.hip", "expert_tile_bias_bf16.hip", "expert_tile_bias_f16.hip",
+           "expert_stream_bias_bf16.hip", "expert_stream_bias_f16.hip", "act_grad.hip", "router_grad.hip",
+           "combine_grad.hip", "grad_norm.hip"]
 # ffn_prefill.hip is compiled once more per block type with only that type's
 # GEMM kernels (QMOE_PREFILL_FMT), so the types compile in parallel.
 PREFILL_TYPES = [1, 2, 3, 4, 5]

@@ -1,0 +1,74 @@
+// The activations of the biased products and their derivatives, fp32, eight
+// values at a time.  SiLU and the tanh form of GELU are both v sigmoid(a v + b v^3):
+// (1 + tanh u) / 2 = sigmoid(2 u).
+#pragma once
+#include "expert_ops.h"
+
+namespace qmoe {
+
+// v held within +-1e4, where every sigmoid is 0 or 1 to the last bit and v^3 is finite; NaN stays.
+__device__ __forceinline__ float act_range(float v) { return v > 1.0e4f ? 1.0e4f : v < -1.0e4f ? -1.0e4f : v; }
+
+constexpr float kGeluA = 1.5957691216057308f;               // 2 sqrt(2 / pi)
+constexpr float kGeluB = 1.5957691216057308f * 0.044715f;
+
+// act(v).
+__device__ __forceinline__ float act1(int act, float v) {
+    if (act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH) {
+        const float b = act == MOE_ACT_SILU ? 0.0f : kGeluB, a = act == MOE_ACT_SILU ? 1.0f : kGeluA, c = act_range(v);
+        return v * sigmoid_f32(c * fmaf(b * c, c, a));
+    }
+    if (act == MOE_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.7071067811865476f));
+    return act == MOE_ACT_RELU && v < 0.0f ? 0.0f : v;
+}
+
+// v = act(v): one test of act for the eight.
+__device__ __forceinline__ void act8(int act, float* v) {
+    if (act == MOE_ACT_NONE) return;
+    if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act1(MOE_ACT_GELU, v[i]);
+    } else if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = act1(MOE_ACT_RELU, v[i]);
+    } else {
+        const float b = act == MOE_ACT_SILU ? 0.0f : kGeluB, a = act == MOE_ACT_SILU ? 1.0f : kGeluA;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = act_range(v[i]);
+            v[i] = v[i] * sigmoid_f32(c * fmaf(b * c, c, a));
+        }
+    }
+}
+
+// dz = d act'(z), h = act(z).
+__device__ __forceinline__ void act_grad8(int act, const float* z, const float* d, float* dz, float* h) {
+    if (act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH) {
+        const bool silu = act == MOE_ACT_SILU;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float c = act_range(z[i]);
+            const float b = silu ? 0.0f : kGeluB, a = silu ? 1.0f : kGeluA;
+            const float u = c * fmaf(b * c, c, a), s = sigmoid_f32(u), q = sigmoid_f32(-u);
+            dz[i] = d[i] * (s * fmaf(c * q, fmaf(3.0f * b * c, c, a), 1.0f));
+            h[i] = z[i] * s;
+        }
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p = 0.5f * (1.0f + erff(z[i] * 0.7071067811865476f));
+            // z e^(-z^2 / 2) / sqrt(2 pi)
+            const float t = -0.7213475204444817f * z[i] * z[i];
+            dz[i] = d[i] * fmaf(z[i], 0.3989422804014327f * __builtin_amdgcn_exp2f(t), p);
+            h[i] = z[i] * p;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            dz[i] = z[i] > 0.0f ? d[i] : 0.0f;
+            h[i] = z[i] < 0.0f ? 0.0f : z[i];
+        }
+    }
+}
+
+}  // namespace qmoe

@@ -31,7 +31,8 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     const int few = tiles <= 64 ? 48 : tiles <= 128 || a.K < 1536 ? 12 : 2;
     if (!a.transpose && a.rows.R <= (long long)few * slots) {
         const StreamArgs t{a.x, a.w, a.w_stride, nullptr, nullptr, 0, 0, a.N, a.K, a.rows, a.x_rows, a.y_rows, a.y,
-                           a.y_dtype == MOE_F32};
+                           a.y_dtype == MOE_F32, 0, 0, a.epilogue ? *a.epilogue : Epilogue{}};
+        if (a.epilogue) return a.dtype == MOE_BF16 ? launch_stream_bias_bf16(t, a.act, s) : launch_stream_bias_f16(t, a.act, s);
         return a.dtype == MOE_BF16 ? launch_stream_bf16(t, 0, a.act, s) : launch_stream_f16(t, 0, a.act, s);
     }
     TileArgs t{};
@@ -40,6 +41,10 @@ hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s) {
     // 256 x 256 tiles once they fill the 256 CUs, else 128 x 128.
     const long long cols = a.transpose ? a.K : a.N;
     const int big = (a.rows.R / 256 + slots) * ((cols + 255) / 256) >= 256;
+    if (a.epilogue) {
+        t.epi = *a.epilogue;
+        return a.dtype == MOE_BF16 ? launch_tile_bias_bf16(t, a.act, big, s) : launch_tile_bias_f16(t, a.act, big, s);
+    }
     const int mode = a.transpose ? kDataGrad : kForward;
     return a.dtype == MOE_BF16 ? launch_tile_bf16(t, mode, a.act, big, s) : launch_tile_f16(t, mode, a.act, big, s);
 }

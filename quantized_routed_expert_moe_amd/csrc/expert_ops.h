@@ -25,6 +25,16 @@ inline RowMap row_map(const int32_t* offsets, const int32_t* perm, int S, int R,
     return {offsets, perm, S, R, k, ((1u << 30) + k - 1) / k};
 }
 
+// What a biased product does behind its sums: z = sum + bias, y = act(z) + residual.
+struct Epilogue {
+    const void* bias;  // [S, N], or NULL
+    int bias_f32;
+    const void* residual;  // as y, or NULL
+    int res_f32;
+    void* z;  // [R, N], or NULL
+    int act;
+};
+
 struct ExpertGemmArgs {
     const void* x;
     const void* w;
@@ -34,6 +44,7 @@ struct ExpertGemmArgs {
     int x_rows, y_rows, act;
     void* y;
     int y_dtype;
+    const Epilogue* epilogue;  // NULL: none but SwiGLU
 };
 hipError_t launch_expert_gemm(const ExpertGemmArgs& a, hipStream_t s);
 

@@ -30,6 +30,7 @@
 #pragma once
 #include <type_traits>
 
+#include "act.h"
 #include "expert_ops.h"
 
 namespace qmoe {
@@ -48,6 +49,7 @@ struct StreamArgs {
     int y_f32;
     int slots;       // slots that can own a position
     int unit_shift;  // a workgroup walks up to 2^unit_shift rows of a slot
+    Epilogue epi;    // biased products
 };
 
 constexpr int kSegment = 256;  // inputs a wave takes at a time
@@ -195,8 +197,8 @@ __device__ __forceinline__ int2 later_unit(const RowMap& m, int e, int shift) {
 // The launch bounds' second number keeps the sums in ordinary registers: the
 // accumulation registers would be read back one by one for the scales.
 // WT 0: 16-bit weights, 1: 4-bit.  SWI: tile 0 holds gate rows, tile 1 the up
-// rows of the same 16 features (NT = 2).
-template <int WT, int DT, int NT, int MB, int PER, bool SWI>
+// rows of the same 16 features (NT = 2).  EPI: the store adds bias and residual.
+template <int WT, int DT, int NT, int MB, int PER, bool SWI, bool EPI>
 __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 : 2) void expert_stream_kernel(const StreamArgs a) {
     typedef typename DType<DT>::type E;
     extern __shared__ float red[];  // [waves][NT][MB][64][4]; before that the table of scales
@@ -447,8 +449,26 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
             const int n = n0 + 16 * t + cc;
             if (n >= width) continue;
             if (WT) v[0] *= 1.0f / kCodeUnit<DT>, v[1] *= 1.0f / kCodeUnit<DT>;
+            const size_t yrow = (size_t)row_of(a.rows, a.y_rows, r.x + rb + row), out = yrow * width + n;
+            if constexpr (EPI) {
+                const size_t at = (size_t)slot * N + n, zat = yrow * N + n;
+                if (a.epi.bias) {
+                    v[0] += a.epi.bias_f32 ? static_cast<const float*>(a.epi.bias)[at] : (float)static_cast<const E*>(a.epi.bias)[at];
+                    if (SWI) v[1] += a.epi.bias_f32 ? static_cast<const float*>(a.epi.bias)[at + half]
+                                                    : (float)static_cast<const E*>(a.epi.bias)[at + half];
+                }
+                if (a.epi.z) {
+                    static_cast<E*>(a.epi.z)[zat] = (E)v[0];
+                    if (SWI) static_cast<E*>(a.epi.z)[zat + half] = (E)v[1];
+                }
+                if (!SWI) v[0] = act1(a.epi.act, v[0]);
+            }
             if (SWI) v[0] = v[0] * sigmoid_f32(v[0]) * v[1];
-            const size_t out = (size_t)row_of(a.rows, a.y_rows, r.x + rb + row) * width + n;
+            if constexpr (EPI) {
+                if (a.epi.residual)
+                    v[0] += a.epi.res_f32 ? static_cast<const float*>(a.epi.residual)[out]
+                                          : (float)static_cast<const E*>(a.epi.residual)[out];
+            }
             if (a.y_f32) static_cast<float*>(a.y)[out] = v[0];
             else static_cast<E*>(a.y)[out] = (E)v[0];
         }
@@ -456,17 +476,17 @@ __global__ __launch_bounds__(64 * kStreamWaves, MB == 4 ? 1 : WT && MB == 1 ? 4 
     }
 }
 
-template <int WT, int DT, int NT, int PER, bool SWI>
+template <int WT, int DT, int NT, int PER, bool SWI, bool EPI>
 static hipError_t stream_launch_rows(const StreamArgs& a, int mb, dim3 grid, int waves, hipStream_t s) {
     const size_t sums = (size_t)waves * NT * mb * 1024, table = WT ? 16 * NT * kTableStride * sizeof(float2) : 0;
     const size_t lds = sums > table ? sums : table;
-    if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else if (mb == 2) expert_stream_kernel<WT, DT, NT, 2, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
-    else if constexpr (PER > 1 && (NT == 1 || SWI)) expert_stream_kernel<WT, DT, NT, 4, PER, SWI><<<grid, 64 * waves, lds, s>>>(a);
+    if (mb == 1) expert_stream_kernel<WT, DT, NT, 1, PER, SWI, EPI><<<grid, 64 * waves, lds, s>>>(a);
+    else if (mb == 2) expert_stream_kernel<WT, DT, NT, 2, PER, SWI, EPI><<<grid, 64 * waves, lds, s>>>(a);
+    else if constexpr (PER > 1 && (NT == 1 || SWI)) expert_stream_kernel<WT, DT, NT, 4, PER, SWI, EPI><<<grid, 64 * waves, lds, s>>>(a);
     return hipGetLastError();
 }
 
-template <int WT, int DT, int PER>
+template <int WT, int DT, int PER, bool EPI = false>
 static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     if (a.rows.R == 0) return hipSuccess;
     const int slots = a.rows.offsets ? (a.rows.R < a.rows.S ? a.rows.R : a.rows.S) : 1;
@@ -497,9 +517,9 @@ static hipError_t stream_launch(const StreamArgs& a, int act, hipStream_t s) {
     const int most = blocks > 3 && blocks > 1 + (long long)columns * slots / 1280 ? 32768 : 1;  // units of a slot
     while ((a.rows.R - 1) >> t.unit_shift >= most) ++t.unit_shift;
     const dim3 grid(columns, slots + ((a.rows.R - 1) >> t.unit_shift));
-    if (act) return stream_launch_rows<WT, DT, 2, PER, true>(t, mb, grid, waves, s);
-    if (few) return stream_launch_rows<WT, DT, 1, PER, false>(t, mb, grid, waves, s);
-    return stream_launch_rows<WT, DT, 2, PER, false>(t, mb, grid, waves, s);
+    if (act) return stream_launch_rows<WT, DT, 2, PER, true, EPI>(t, mb, grid, waves, s);
+    if (few) return stream_launch_rows<WT, DT, 1, PER, false, EPI>(t, mb, grid, waves, s);
+    return stream_launch_rows<WT, DT, 2, PER, false, EPI>(t, mb, grid, waves, s);
 }
 
 template <int DT>
@@ -512,6 +532,8 @@ static hipError_t stream_launch_type(const StreamArgs& a, int w4, int act, hipSt
     }
 }
 
+hipError_t launch_stream_bias_bf16(const StreamArgs& a, int act, hipStream_t s);
+hipError_t launch_stream_bias_f16(const StreamArgs& a, int act, hipStream_t s);
 hipError_t launch_stream_bf16(const StreamArgs& a, int w4, int act, hipStream_t s);
 hipError_t launch_stream_f16(const StreamArgs& a, int w4, int act, hipStream_t s);
 

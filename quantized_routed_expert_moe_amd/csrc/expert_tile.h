@@ -40,6 +40,7 @@
 #pragma once
 #include <type_traits>
 
+#include "act.h"
 #include "expert_ops.h"
 
 namespace qmoe {
@@ -56,6 +57,7 @@ struct TileArgs {
     int y_f32;
     int splits;       // weight gradient: parts of a slot's rows
     int group;        // column tiles of a group
+    Epilogue epi;     // biased products
 };
 
 enum { kForward = 0, kDataGrad = 1, kWeightGrad = 2 };
@@ -87,11 +89,11 @@ __device__ __forceinline__ uint2 pack4(const float* v) {
     return __builtin_bit_cast(uint2, u);
 }
 
-// QI x PI blocks of 32 x 32 a wave, WQ x WP waves.
-template <int DT_, int MODE_, bool SWI_, int QI_, int PI_, int WQ_, int WP_>
+// QI x PI blocks of 32 x 32 a wave, WQ x WP waves.  EPI: the store adds bias and residual.
+template <int DT_, int MODE_, bool SWI_, int QI_, int PI_, int WQ_, int WP_, bool EPI_ = false>
 struct Tile {
     static constexpr int DT = DT_, MODE = MODE_, QI = QI_, PI = PI_, WQ = WQ_, WP = WP_, NBUF = 2;
-    static constexpr bool SWI = SWI_;
+    static constexpr bool SWI = SWI_, EPI = EPI_;
     static constexpr int BK = 64;
     static constexpr int W = WQ * WP, THREADS = 64 * W;
     static constexpr int BQ = 32 * QI * WQ, BP = 32 * PI * WP;
@@ -503,6 +505,121 @@ __device__ __forceinline__ void tile_store(const TileArgs& a, int slot, int q0, 
     }
 }
 
+// LDS accesses of a wave's lanes before it come before those behind it: the hardware
+// takes a wave's in order, the compiler is kept from moving them.
+__device__ __forceinline__ void wave_lds_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Eight elements of a row: fp32 or the tile's type.
+template <int DT>
+__device__ __forceinline__ void load8_of(const void* p, int f32, size_t at, float* v) {
+    if (f32) load_vec8<MOE_F32>(p, at, v);
+    else load_vec8<DT>(p, at, v);
+}
+
+// tile_store of a biased product.  32 rows of the wave's 64 columns at a time lie in its
+// share of the stage buffers as fp32; a lane takes eight columns of a row, whose bias it holds
+// in registers.  First z and the activation, in place, in a loop that is not unrolled (erf and
+// the rest would be repeated 40 times in the code); then residual, rounding and store, the
+// residual's rows requested before the first part.
+template <typename C, int NB>
+__device__ __forceinline__ void tile_store_epilogue(const TileArgs& a, int slot, int q0, int nq, int p0,
+                                                    const TileLds<C>& lds, const f32x16 (&acc)[NB][C::PI]) {
+    static_assert(C::MODE == kForward && C::PI == 2, "64 columns a wave");
+    constexpr int DT = C::DT, WQ = C::WQ, STRIDE = 64 + 4, SHARE = 32 * STRIDE * 4;
+    constexpr int PER = C::QBYTES / SHARE, LANES = C::SWI ? 4 : 8, AT = 64 / LANES, STEPS = 32 / AT;
+    static_assert(C::QBYTES == C::PBYTES && C::W <= PER * 2 * C::NBUF, "a share for each wave");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wq = wave % WQ, wp = wave / WQ, N = a.N, width = C::SWI ? N / 2 : N;
+    uint8_t* buf[4] = {lds.q[0], lds.q[1], lds.p[0], lds.p[1]};
+    float* mine = nullptr;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        if (wave >= u * PER && wave < (u + 1) * PER) mine = reinterpret_cast<float*>(buf[u] + (wave - u * PER) * SHARE);
+    const Epilogue& e = a.epi;
+    const int piece = lane % LANES, c = p0 + wp * (C::SWI ? 32 : 64) + piece * 8;
+    const bool in = c < width, early = C::SWI || e.act != MOE_ACT_NONE || e.z;
+    float bias[C::SWI ? 16 : 8] = {};
+    if (e.bias && in) {
+        load8_of<DT>(e.bias, e.bias_f32, (size_t)slot * N + c, bias);
+        if constexpr (C::SWI) load8_of<DT>(e.bias, e.bias_f32, (size_t)slot * N + width + c, bias + 8);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int base = 32 * (wq + WQ * b);
+        if (base >= nq) continue;
+        size_t row[STEPS];
+        bool live[STEPS];
+        float res[STEPS][8];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int r = base + i * AT + lane / LANES;
+            live[i] = in && r < nq;
+            row[i] = (size_t)row_of(a.rows, a.y_rows, q0 + min(r, nq - 1));
+            if (e.residual && live[i]) load8_of<DT>(e.residual, e.res_f32, row[i] * width + c, res[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x16 v = acc[b][j];
+                *reinterpret_cast<float4*>(mine + (lane & 31) * STRIDE + 32 * j + 8 * g + 4 * (lane >> 5)) =
+                    make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+            }
+        wave_lds_order();
+        if (early) {
+#pragma unroll 1
+            for (int i = 0; i < STEPS; ++i) {
+                const int r = i * AT + lane / LANES;
+                float* at = mine + r * STRIDE + piece * 8;
+                float v[8];
+                load_vec8<MOE_F32>(at, 0, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += bias[j];
+                const bool store = e.z && in && base + r < nq;
+                size_t out = 0;
+                if (store) {
+                    out = (size_t)row_of(a.rows, a.y_rows, q0 + base + r) * N + c;
+                    store_vec8<DT>(e.z, out, v);
+                }
+                if constexpr (C::SWI) {
+                    float u[8];
+                    load_vec8<MOE_F32>(at + 32, 0, u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[j] += bias[8 + j];
+                    if (store) store_vec8<DT>(e.z, out + width, u);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid_f32(v[j]) * u[j];
+                } else {
+                    act8(e.act, v);
+                }
+                store_vec8<MOE_F32>(at, 0, v);
+            }
+            wave_lds_order();
+        }
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            float v[8];
+            load_vec8<MOE_F32>(mine + (i * AT + lane / LANES) * STRIDE + piece * 8, 0, v);
+            if (!live[i]) continue;
+            if (!early) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += bias[j];
+            }
+            if (e.residual) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += res[i][j];
+            }
+            if (a.y_f32) store_vec8<MOE_F32>(a.y, row[i] * width + c, v);
+            else store_vec8<DT>(a.y, row[i] * width + c, v);
+        }
+        wave_lds_order();
+    }
+}
+
 // Row tile `index` of the batch, slots in order: whole tiles (bound by the
 // matrix cores) and rests (bound by the weights' stream) alternate, which
 // measured 13 % faster than all whole tiles first.  Found by one scan over
@@ -601,7 +718,8 @@ __global__ __launch_bounds__(C::THREADS, C::QI * C::PI == 4 ? 2 : 1) void expert
         constexpr int NB = decltype(tag)::value;
         f32x16 acc[NB][C::PI] = {};
         tile_product<C, NB>(a, slot, q0, nq, c0, p0, len, lds, acc);
-        tile_store<C, NB>(a, slot, q0, nq, p0, lds, acc);
+        if constexpr (C::EPI) tile_store_epilogue<C, NB>(a, slot, q0, nq, p0, lds, acc);
+        else tile_store<C, NB>(a, slot, q0, nq, p0, lds, acc);
     };
     constexpr int QI = C::QI;
     if (C::MODE == kWeightGrad || nb == QI) body(std::integral_constant<int, QI>{});
@@ -632,9 +750,10 @@ static hipError_t tile_launch(const TileArgs& a, hipStream_t s) {
 }
 
 // 256 x 256 by eight waves of 128 x 64, 128 x 128 by four of 64 x 64.
-template <int DT, int MODE, bool SWI>
+template <int DT, int MODE, bool SWI, bool EPI = false>
 static hipError_t tile_launch_size(const TileArgs& a, int big, hipStream_t s) {
-    return big ? tile_launch<Tile<DT, MODE, SWI, 4, 2, 2, 4>>(a, s) : tile_launch<Tile<DT, MODE, SWI, 2, 2, 2, 2>>(a, s);
+    return big ? tile_launch<Tile<DT, MODE, SWI, 4, 2, 2, 4, EPI>>(a, s)
+               : tile_launch<Tile<DT, MODE, SWI, 2, 2, 2, 2, EPI>>(a, s);
 }
 
 template <int DT>
@@ -644,6 +763,13 @@ static hipError_t tile_launch_type(const TileArgs& a, int mode, int act, int big
     return tile_launch_size<DT, kWeightGrad, false>(a, big, s);
 }
 
+template <int DT>
+static hipError_t tile_launch_bias(const TileArgs& a, int act, int big, hipStream_t s) {
+    return act ? tile_launch_size<DT, kForward, true, true>(a, big, s) : tile_launch_size<DT, kForward, false, true>(a, big, s);
+}
+
+hipError_t launch_tile_bias_bf16(const TileArgs& a, int act, int big, hipStream_t s);
+hipError_t launch_tile_bias_f16(const TileArgs& a, int act, int big, hipStream_t s);
 hipError_t launch_tile_bf16(const TileArgs& a, int mode, int act, int big, hipStream_t s);
 hipError_t launch_tile_f16(const TileArgs& a, int mode, int act, int big, hipStream_t s);
 

@@ -1,0 +1,146 @@
+// Internal declarations of the operators of a training step: the activations'
+// and biases' gradients, the router's losses and gradient, the combine's
+// gradient, the gradient norm and clipping; and the device helpers they share.
+#pragma once
+#include "device_common.h"
+#include "expert_ops.h"
+
+namespace qmoe {
+
+struct ActGradArgs {
+    const void* dy;
+    const void* z;
+    int dtype, N;
+    RowMap rows;
+    int how, act;
+    void* dz;
+    void* h;
+    float* dbias;
+    void* ws;
+};
+size_t act_grad_workspace_bytes(int S, int N, int R);
+hipError_t launch_act_grad(const ActGradArgs& a, hipStream_t s);
+
+struct RouterArgs {
+    const float* logits;
+    const int32_t* ids;
+    int T, E, k, score;
+    RowMap seqs;  // offsets of the G sequences
+    // losses
+    int32_t* counts_out;
+    float* probs;
+    float* losses;
+    void* ws;
+    // gradient
+    const float* dw;
+    int renormalize;
+    float scale;
+    const int32_t* counts;
+    const float* dlosses;
+    void* dlogits;
+    int out_dtype;
+};
+size_t balance_loss_workspace_bytes(int T, int E, int G);
+hipError_t launch_balance_loss(const RouterArgs& a, hipStream_t s);
+hipError_t launch_route_backward(const RouterArgs& a, hipStream_t s);
+
+struct CombineGradArgs {
+    const void* dy;
+    int dy_dtype;
+    const void* y_pairs;
+    int pairs_dtype;
+    const int32_t* ids;
+    const float* w;
+    const int32_t* slot_of_expert;
+    int E, S, T, k, H;
+    void* dy_pairs;
+    float* dw;
+};
+hipError_t launch_combine_backward(const CombineGradArgs& a, hipStream_t s);
+
+struct GradListArgs {
+    const void* const* grads;
+    const int64_t* counts;
+    const int32_t* dtypes;
+    void* const* outs;  // clipping; NULL: in place
+    const int32_t* out_dtypes;
+    int n, kind;
+    float scale, max_norm, eps;
+    float* total;
+    void* ws;
+};
+size_t grad_norm_workspace_bytes(int n);
+hipError_t launch_grad_norm(const GradListArgs& a, hipStream_t s);
+hipError_t launch_grad_clip(const GradListArgs& a, hipStream_t s);
+
+#ifdef __HIPCC__
+
+// e^x.  log2(e) x is split into its rounded value and the rest, as in
+// sigmoid_f32; 0 below the range, -inf included.
+__device__ __forceinline__ float exp_f32(float x) {
+    const float t = 1.4426950408889634f * x;
+    const float rest = fmaf(1.4426950408889634f, x, -t) + 1.925963033500e-8f * x;
+    const float e = __builtin_amdgcn_exp2f(t);
+    return e > 0.0f && e < 3.0e38f ? fmaf(e, 0.6931471805599453f * rest, e) : e;
+}
+
+// Largest value of the wave, in every lane (NaN is passed over).
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+    return v;
+}
+
+// Part `index` of the slots' rows, cut into parts of `per` rows each, slots in
+// order: its slot, first position and rows.  Found by one scan over the slots
+// (S <= 1024) of the whole workgroup; false if there are fewer parts.  prefix, if
+// not NULL, receives the parts before each slot, [S + 1].
+template <int THREADS>
+__device__ __forceinline__ bool find_part(const RowMap& m, int per, int index, int32_t* prefix, int& slot, int& q0,
+                                          int& nq) {
+    __shared__ int wsum[THREADS / 64], found[3];
+    constexpr int PER = 1024 / THREADS;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    int2 r[PER];
+    int parts = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int s = t * PER + j;
+        r[j] = s < m.S ? slot_range(m, s) : make_int2(0, 0);
+        parts += (r[j].y + per - 1) / per;
+    }
+    int sum = parts;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int x = __shfl_up(sum, o, 64);
+        if (lane >= o) sum += x;
+    }
+    if (lane == 63) wsum[wave] = sum;
+    if (t == 0) found[0] = -1;
+    __syncthreads();
+    sum -= parts;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w)
+        if (w < wave) sum += wsum[w];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int s = t * PER + j, n = (r[j].y + per - 1) / per, at = index - sum;
+        if (prefix && s <= m.S) prefix[s] = sum;
+        if (at >= 0 && at < n) {
+            found[0] = s;
+            found[1] = r[j].x + at * per;
+            found[2] = min(per, r[j].y - at * per);
+        }
+        sum += n;
+    }
+    if (prefix && m.S == 1024 && t == THREADS - 1) prefix[m.S] = sum;
+    __syncthreads();
+    slot = __builtin_amdgcn_readfirstlane(found[0]);
+    q0 = __builtin_amdgcn_readfirstlane(found[1]);
+    nq = __builtin_amdgcn_readfirstlane(found[2]);
+    return slot >= 0;
+}
+
+#endif  // __HIPCC__
+
+}  // namespace qmoe
