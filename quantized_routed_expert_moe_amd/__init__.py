@@ -8,6 +8,7 @@ the library is not built the first call raises; there is no fallback.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 import re
@@ -881,7 +882,7 @@ class moe_tensor_list:
         for (_, end), (start, _) in zip(self.ranges, self.ranges[1:]):
             if start < end:
                 raise ValueError("two tensors of the list overlap")
-        self.n, self.total, self.counts, self.codes, self.at = n, sum(counts), counts, codes, at
+        self.n, self.counts, self.codes, self.at, self.apart = n, counts, codes, at, None
         self.c_at, self.c_counts, self.c_codes = (ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*counts), \
             (ctypes.c_int32 * n)(*codes)
 
@@ -890,7 +891,7 @@ class moe_tensor_list:
 
 
 def _op_list(tensors, device: int) -> moe_tensor_list:
-    lst = tensors if isinstance(tensors, moe_tensor_list) else moe_tensor_list(tensors)
+    lst = tensors if type(tensors) is moe_tensor_list else moe_tensor_list(tensors)
     if lst.device != device:
         raise TypeError(f"the list's tensors must be on the current device (cuda:{device})")
     return lst
@@ -919,7 +920,7 @@ def moe_grad_norm(grads, total, kind: int = MOE_NORM_L2, scale: float = 1.0, ws=
 
 
 def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float = 1.0, outs=None, stream=None):
-    """grads times scale min(1, max_norm / (total + eps)), in place or into outs (the same shapes, any of the types)."""
+    """grads times scale min(1, max_norm / (total + eps)), in place or into outs (the same sizes, any of the types)."""
     dev = _op_device()
     lst = _op_list(grads, dev)
     _op_total(total)
@@ -927,34 +928,29 @@ def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float
     op = oc = None
     if outs is not None:
         out = _op_list(outs, dev)
-        if out.counts != lst.counts:
-            raise ValueError("outs must have the sizes of grads")
-        _op_apart(lst, out)
+        if lst.apart is not out:
+            _op_apart(lst, out)
         op, oc = out.c_at, out.c_codes
     _check(lib().moe_grad_clip(lst.c_at, lst.c_counts, lst.c_codes, op, oc, lst.n, tp, float(max_norm), float(eps),
                                float(scale), _op_stream(dev, stream)))
 
 
 def _op_apart(lst: moe_tensor_list, out: moe_tensor_list) -> None:
-    """Every output is its own gradient or overlaps none."""
-    if out is lst or out.at == lst.at:
-        if out.codes != lst.codes:
-            raise ValueError("an output is its gradient in another type")
-        return
-    own = {a: code for a, c, code in zip(lst.at, lst.counts, lst.codes) if c}
-    for i, (a, c) in enumerate(zip(out.at, out.counts)):
-        if c and a == lst.at[i]:
-            if out.codes[i] != own[a]:
-                raise ValueError("an output is its gradient in another type")
+    """Every output is its own gradient or overlaps none.  Lists do not change, so a pair of them is looked at once."""
+    if out.counts != lst.counts:
+        raise ValueError("outs must have the sizes of grads")
     starts = [r[0] for r in lst.ranges]
-    import bisect
-    for i, (a, c, code) in enumerate(zip(out.at, out.counts, out.codes)):
-        if not c or a == lst.at[i]:
+    for a, c, code, own, own_code in zip(out.at, out.counts, out.codes, lst.at, lst.codes):
+        if not c:
             continue
-        end = a + c * (4 if code == MOE_F32 else 2)
-        j = bisect.bisect_left(starts, end)
+        if a == own:
+            if code != own_code:
+                raise ValueError("an output is its gradient in another type")
+            continue
+        j = bisect.bisect_left(starts, a + c * (4 if code == MOE_F32 else 2))
         if j and lst.ranges[j - 1][1] > a:
             raise ValueError("an output overlaps another gradient")
+    lst.apart = out
 
 
 # ------------------------------------------------------------ host leg
