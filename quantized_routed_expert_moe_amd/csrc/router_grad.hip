@@ -1,73 +1,95 @@
 // The router's balance loss, z loss and per-expert counts over ragged
 // sequences, and the gate logits' gradient.
 //
-// A wave owns a row: its E <= 1024 logits sit in registers, so the largest logit,
-// the sums and the probabilities come out of one read.  Rows are a few KB, so
-// short calls are latency and long ones HBM (logits once, and the gradient once).
+// 16 lanes own a row of up to 256 logits, 64 a wider one: it sits in registers, so the
+// largest logit, the sums and the probabilities come out of one read, and a sum over a row is
+// four steps between lanes for four rows at a time (with 64 lanes for every row the gradient of
+// 16384 rows of 256 took 18 us: the vector units' time, not the memory's, which is 5 us).
 // The probabilities' means are sums over rows in registers, joined over a workgroup's
 // waves in LDS, then over workgroups by a second launch in their order: no atomics on
 // floats (the counts' are on integers in LDS).
 //
-// With m the row's largest logit, s = sigmoid(l) and e = e^(l - m), the
-// probabilities are e / sum e, or s / sum s.  The latter is taken as r / sum r with
-// r = s for m >= 0 and r = e sigmoid(-l) = s e^-m for m < 0: rows of low logits
-// would underflow in s.
+// With m the row's largest logit and e = e^(l - m), the probabilities are e / sum e, or
+// s / sum s with s = t / (1 + t), t = e e^m: one exponential for both.  The latter is taken as
+// r / sum r with r = s for m >= 0 and r = e / (1 + t) = s e^-m for m < 0: rows of low
+// logits would underflow in s.
 #include "train_ops.h"
 
 namespace qmoe {
 
 constexpr int kLossWaves = 16, kLossThreads = 64 * kLossWaves;
 
-// A row in registers: register i of lane l holds element ((i / VEC) * 64 + l) * VEC + i % VEC.
+// A row over L lanes: register i of lane l holds element ((i / VEC) * L + l) * VEC + i % VEC.
 // VEC = 4 takes 16-byte loads (E a multiple of 4).
-template <int VEC, int NV>
+template <int L_, int VEC_, int NV_>
 struct Row {
-    static constexpr int N = VEC * NV;
-    static __device__ __forceinline__ int element(int i, int lane) { return ((i / VEC) * 64 + lane) * VEC + i % VEC; }
-    static __device__ __forceinline__ void load(const float* row, int E, int lane, float* v) {
+    static constexpr int L = L_, VEC = VEC_, NV = NV_, N = VEC * NV, ROWS = 64 / L;  // rows of a wave
+    static __device__ __forceinline__ int element(int i, int lane) { return ((i / VEC) * L + lane) * VEC + i % VEC; }
+    template <typename T>
+    static __device__ __forceinline__ void load(const T* row, int E, int lane, T rest, T* v) {
+        typedef T vec __attribute__((ext_vector_type(VEC)));
 #pragma unroll
         for (int g = 0; g < NV; ++g) {
             const int e = element(g * VEC, lane);
-            if constexpr (VEC == 4) {
-                const float4 q = e < E ? *reinterpret_cast<const float4*>(row + e)
-                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                v[4 * g] = q.x; v[4 * g + 1] = q.y; v[4 * g + 2] = q.z; v[4 * g + 3] = q.w;
-            } else {
-                v[g] = e < E ? row[e] : -INFINITY;
-            }
+            vec q;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) q[c] = rest;
+            if (e < E) q = *reinterpret_cast<const vec*>(row + e);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) v[g * VEC + c] = q[c];
         }
     }
 };
 
-// Probabilities of a row.  p: as above; soft: softmax (of SIGMOID rows too), e^(l - top) inv;
-// lse: log of the sum of e^l.  Registers behind the row hold -inf and come out as 0.
-template <int N, bool SIGMOID>
-__device__ __forceinline__ void probabilities(const float* l, float* p, float* soft, float& lse, float& top, float& inv) {
-    float m = l[0];
+struct RowSums {
+    float m, top;     // largest logit; 0 for -inf (a row of nothing)
+    float inv, rinv;  // 1 / sum e, 1 / sum r (0 for a row of nothing)
+    float lse;
+};
+
+// r of one logit given e, and 1 - s.
+template <bool SIGMOID>
+__device__ __forceinline__ float score_of(float l, float e, float em, bool far, float m, float& q) {
+    if (!SIGMOID) {
+        q = 1.0f;
+        return e;
+    }
+    const float t = far ? exp_f32(l) : e * em;  // far: e^m, or what e lost below e^-104, matters
+    q = __builtin_amdgcn_rcpf(1.0f + t);
+    return m < 0.0f ? e * q : t > 1.0f ? 1.0f - q : t * q;
+}
+
+// Of a row's logits l: e, r (SIGMOID; else r is e) and q = 1 - s.  Registers behind the row hold -inf.
+template <typename R, bool SIGMOID>
+__device__ __forceinline__ RowSums probabilities(const float* l, float* e, float* r, float* q) {
+    RowSums s;
+    s.m = l[0];
 #pragma unroll
-    for (int i = 1; i < N; ++i) m = fmaxf(m, l[i]);
-    m = wave_max(m);
-    top = m == -INFINITY ? 0.0f : m;  // a row of nothing
+    for (int i = 1; i < R::N; ++i) s.m = fmaxf(s.m, l[i]);
+    s.m = lanes_max<R::L>(s.m);
+    s.top = s.m == -INFINITY ? 0.0f : s.m;
+    const bool far = SIGMOID && __any(s.top > 40.0f);
+    const float em = SIGMOID ? exp_f32(s.top) : 0.0f;
     float sum = 0.0f, rsum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        soft[i] = exp_f32(l[i] - top);
-        sum += soft[i];
-        if (SIGMOID) {
-            p[i] = m < 0.0f ? soft[i] * sigmoid_f32(-l[i]) : sigmoid_f32(l[i]);
-            rsum += p[i];
-        }
+    for (int i = 0; i < R::N; ++i) {
+        e[i] = exp_down(l[i] - s.top);
+        sum += e[i];
     }
-    sum = wave_sum(sum);
-    lse = sum == 0.0f ? 0.0f : top + logf(sum);
-    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (SIGMOID) rsum = wave_sum(rsum);
-    const float rinv = rsum == 0.0f ? 0.0f : 1.0f / rsum;
+    if (SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        soft[i] *= inv;
-        p[i] = SIGMOID ? p[i] * rinv : soft[i];
+        for (int i = 0; i < R::N; ++i) {
+            r[i] = score_of<true>(l[i], e[i], em, far, s.m, q[i]);
+            rsum += r[i];
+        }
+        rsum = lanes_sum<R::L>(rsum);
+        s.rinv = rsum == 0.0f ? 0.0f : 1.0f / rsum;
     }
+    sum = lanes_sum<R::L>(sum);
+    s.inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    s.lse = sum == 0.0f ? 0.0f : s.top + logf(sum);
+    if (!SIGMOID) s.rinv = s.inv;
+    return s;
 }
 
 struct LossParts {  // the workspace: parts of the rows, [parts][E] sums and counts, [parts] sums of lse^2
@@ -102,12 +124,12 @@ __device__ __forceinline__ float group_sum(float v) {
 
 // One part of the rows: sums of the probabilities, counts and sum of lse^2.
 // ALONE: there is one part only, and the workgroup writes the results.
-template <int VEC, int NV, bool SIGMOID, bool ALONE>
+template <typename R, bool SIGMOID, bool ALONE>
 __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArgs a, const LossParts ws) {
-    typedef Row<VEC, NV> R;
-    __shared__ float join[kLossWaves * R::N * 64];
+    constexpr int WIDE = R::N * R::L;  // elements that the registers hold
+    __shared__ float join[kLossWaves * WIDE];
     __shared__ int hist[1024];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.E;
+    const int lane = threadIdx.x % R::L, unit = threadIdx.x / R::L, wave = threadIdx.x >> 6, E = a.E;
     hist[threadIdx.x] = 0;
     int seq, q0, nq;
     const bool any = find_part<kLossThreads>(a.seqs, ws.per, blockIdx.x, blockIdx.x == 0 && !ALONE ? ws.prefix : nullptr,
@@ -117,13 +139,16 @@ __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArg
         q0 = nq = 0;
     }
     float acc[R::N] = {}, z = 0.0f;
-    for (int r = wave; r < nq; r += kLossWaves) {
-        float l[R::N], p[R::N], soft[R::N], lse, top, inv;
-        R::load(a.logits + (size_t)(q0 + r) * E, E, lane, l);
-        probabilities<R::N, SIGMOID>(l, p, soft, lse, top, inv);
+    for (int r0 = 0; r0 < nq; r0 += kLossWaves * R::ROWS) {
+        const int row = r0 + unit;
+        const bool live = row < nq;
+        float l[R::N], e[R::N], r[R::N], q[R::N];
+        R::load(a.logits + (size_t)(q0 + min(row, nq - 1)) * E, E, lane, -INFINITY, l);
+        const RowSums s = probabilities<R, SIGMOID>(l, e, r, q);
+        const float inv = live ? s.rinv : 0.0f;
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) acc[i] += p[i];
-        z = fmaf(lse, lse, z);
+        for (int i = 0; i < R::N; ++i) acc[i] += live ? (SIGMOID ? r[i] : e[i]) * inv : 0.0f;
+        z = live ? fmaf(s.lse, s.lse, z) : z;
     }
     const int32_t* ids = a.ids + (size_t)q0 * a.k;
     for (int i = threadIdx.x; i < nq * a.k; i += kLossThreads) {
@@ -131,13 +156,16 @@ __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArg
         if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
     }
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) join[wave * R::N * 64 + R::element(i, lane)] = acc[i];
+    for (int i = 0; i < R::N; ++i) {
+        const float v = R::L == 16 ? sum_of_rows(acc[i]) : acc[i];
+        if (R::L == 64 || (threadIdx.x & 63) < 16) join[wave * WIDE + R::element(i, lane)] = v;
+    }
     z = group_sum<kLossWaves>(lane == 0 ? z : 0.0f);
     __syncthreads();
     const int e = threadIdx.x;
     float sum = 0.0f;
     if (e < E)
-        for (int w = 0; w < kLossWaves; ++w) sum += join[w * R::N * 64 + e];
+        for (int w = 0; w < kLossWaves; ++w) sum += join[w * WIDE + e];
     if (ALONE) {
         const float mean = nq > 0 ? sum / (float)nq : 0.0f;
         const float balance = group_sum<kLossWaves>(e < E ? (float)hist[e] * mean : 0.0f);
@@ -234,31 +262,33 @@ size_t balance_loss_workspace_bytes(int T, int E, int G) {
     return bytes;
 }
 
-template <int VEC, int NV>
+template <typename R>
 static void launch_loss_rows(const RouterArgs& a, const LossParts& ws, bool alone, hipStream_t s) {
     const dim3 grid(alone ? 1 : ws.parts);
     if (a.score == MOE_SCORE_SIGMOID) {
-        if (alone) loss_rows_kernel<VEC, NV, true, true><<<grid, kLossThreads, 0, s>>>(a, ws);
-        else loss_rows_kernel<VEC, NV, true, false><<<grid, kLossThreads, 0, s>>>(a, ws);
+        if (alone) loss_rows_kernel<R, true, true><<<grid, kLossThreads, 0, s>>>(a, ws);
+        else loss_rows_kernel<R, true, false><<<grid, kLossThreads, 0, s>>>(a, ws);
     } else {
-        if (alone) loss_rows_kernel<VEC, NV, false, true><<<grid, kLossThreads, 0, s>>>(a, ws);
-        else loss_rows_kernel<VEC, NV, false, false><<<grid, kLossThreads, 0, s>>>(a, ws);
+        if (alone) loss_rows_kernel<R, false, true><<<grid, kLossThreads, 0, s>>>(a, ws);
+        else loss_rows_kernel<R, false, false><<<grid, kLossThreads, 0, s>>>(a, ws);
     }
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// launch<VEC, NV>() of the smallest row that holds E logits.
+// launch(Row) with the smallest row that holds E logits.
 template <typename F>
 static void by_width(int E, bool wide, F&& launch) {
     if (wide) {
-        if (E <= 256) launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 1>{});
-        else if (E <= 512) launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-        else launch(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+        if (E <= 64) launch(Row<16, 4, 1>{});
+        else if (E <= 128) launch(Row<16, 4, 2>{});
+        else if (E <= 256) launch(Row<16, 4, 4>{});
+        else if (E <= 512) launch(Row<64, 4, 2>{});
+        else launch(Row<64, 4, 4>{});
     } else {
-        if (E <= 64) launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
-        else if (E <= 256) launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-        else launch(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
+        if (E <= 64) launch(Row<16, 1, 4>{});
+        else if (E <= 256) launch(Row<16, 1, 16>{});
+        else launch(Row<64, 1, 16>{});
     }
 }
 
@@ -266,9 +296,7 @@ hipError_t launch_balance_loss(const RouterArgs& a, hipStream_t s) {
     const int G = a.seqs.S, groups = (a.E + 63) / 64;
     const LossParts ws = loss_parts(a.T, a.E, G, a.ws, nullptr);
     const bool alone = G == 1 && a.T <= ws.per;
-    by_width(a.E, a.E % 4 == 0 && aligned16(a.logits), [&](auto vec, auto nv) {
-        launch_loss_rows<decltype(vec)::value, decltype(nv)::value>(a, ws, alone, s);
-    });
+    by_width(a.E, a.E % 4 == 0 && aligned16(a.logits), [&](auto row) { launch_loss_rows<decltype(row)>(a, ws, alone, s); });
     if (!alone) {
         loss_join_kernel<<<dim3(G, groups), 1024, 0, s>>>(a, ws);
         loss_sum_kernel<<<1, 1024, 0, s>>>(a, ws, groups);
@@ -278,110 +306,180 @@ hipError_t launch_balance_loss(const RouterArgs& a, hipStream_t s) {
 
 // --------------------------------------------------------------- gradient
 
-// Sequence of row t: the last one that begins at or before it, -1 if it lies in none.
-__device__ __forceinline__ int sequence_of(const RowMap& m, int t, int lane) {
+// Sequences of the rows t0 .. t0 + ROWS of a wave, that of this lane's row: the last one that
+// begins at or before it, -1 if it lies in none.
+template <typename R>
+__device__ __forceinline__ int sequence_of(const RowMap& m, int t0) {
     if (!m.offsets) return 0;
-    int before = 0;
+    const int lane = threadIdx.x & 63;
+    int before[R::ROWS] = {};
     for (int s0 = 0; s0 <= m.S; s0 += 64) {
-        const int s = s0 + lane;
-        before += __popcll(__ballot(s <= m.S && m.offsets[min(s, m.S)] <= t));
+        const int s = s0 + lane, at = m.offsets[min(s, m.S)];
+#pragma unroll
+        for (int r = 0; r < R::ROWS; ++r) before[r] += __popcll(__ballot(s <= m.S && at <= t0 + r));
     }
-    return before >= 1 && before <= m.S ? before - 1 : -1;
+    int mine = before[0];
+#pragma unroll
+    for (int r = 1; r < R::ROWS; ++r) mine = lane / R::L == r ? before[r] : mine;
+    return mine >= 1 && mine <= m.S ? mine - 1 : -1;
 }
 
-// A wave a row.  Lane j < k holds pair j; the pairs' terms go to their logits' registers
-// one by one.
-template <int VEC, int NV, bool SIGMOID, int OUT>
+// f(integral constants 0 .. N - 1).
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void unrolled(F&& f) {
+    if constexpr (I < N) {
+        f(std::integral_constant<int, I>{});
+        unrolled<N, I + 1>(f);
+    }
+}
+
+// The lanes write the row's gradient through the losses (and, of a softmax that is not
+// renormalised, the pull of the weights' sum); then lane j of them, which holds pair j (and j + L,
+// ...), writes its expert's logit once more, with all that comes from the pairs of this
+// expert, and the rest computed again from the logit.  (Adding the pairs' terms to the registers
+// that hold their logits took a third of the kernel.)  A wave's stores to one place are made in
+// their order.
+template <typename R, int KP, bool SIGMOID, int OUT>
 __global__ __launch_bounds__(256) void route_grad_kernel(const RouterArgs a) {
-    typedef Row<VEC, NV> R;
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), E = a.E;
-    if (t >= a.T) return;
+    constexpr int N = R::N, L = R::L;
+    const int lane = threadIdx.x % L, E = a.E, k = a.k;
+    const int t0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * R::ROWS;
+    if (t0 >= a.T) return;
+    const bool live = t0 + (int)(threadIdx.x & 63) / L < a.T;
+    const int t = min(t0 + (int)(threadIdx.x & 63) / L, a.T - 1);
     const float* row = a.logits + (size_t)t * E;
-    const int seq = a.counts ? sequence_of(a.seqs, t, lane) : -1;
-    const bool whole = seq >= 0 || (a.dw && !SIGMOID && !a.renormalize);  // all logits count
-    float d[R::N], p[R::N], soft[R::N], l[R::N], lse = 0.0f, top = 0.0f, inv = 0.0f;
+    const bool pull = a.dw && !SIGMOID && !a.renormalize;  // the weights depend on all logits
+    const bool whole = a.counts || pull;
+
+    // the pairs
+    int id[KP];
+    float dw[KP], z[KP];
+    bool valid[KP];
 #pragma unroll
-    for (int i = 0; i < R::N; ++i) d[i] = 0.0f;
+    for (int u = 0; u < KP; ++u) {
+        const int j = u * L + lane;
+        id[u] = a.dw && j < k ? a.ids[(size_t)t * k + j] : -1;
+        valid[u] = id[u] >= 0 && id[u] < E;
+        dw[u] = valid[u] ? a.scale * a.dw[(size_t)t * k + j] : 0.0f;
+        z[u] = valid[u] ? row[id[u]] : -INFINITY;
+    }
+    float l[N], e[N], r[N], q[N], f[N];
+    RowSums s = {};
+    int seq = -1;
+    float b = 0.0f, zs = 0.0f, em = 0.0f, dot = 0.0f, draw = 0.0f;
+    const int32_t* counts = a.counts;
+    if (whole) R::load(row, E, lane, -INFINITY, l);
+    if (a.counts) {
+        seq = sequence_of<R>(a.seqs, t0);
+        counts += (size_t)max(seq, 0) * E;
+        int32_t c[N];
+        R::load(counts, E, lane, 0, c);
+        const float n = (float)rows_of_all(a.seqs), ng = (float)slot_range(a.seqs, max(seq, 0)).y;
+        b = a.dlosses[0] * ((float)E / ((float)k * n)) / ng;
+        zs = a.dlosses[1] * (2.0f / n);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = (float)c[i];
+    }
+    bool far = false;
     if (whole) {
-        R::load(row, E, lane, l);
-        probabilities<R::N, SIGMOID>(l, p, soft, lse, top, inv);
+        s = probabilities<R, SIGMOID>(l, e, r, q);
+        em = SIGMOID ? exp_f32(s.top) : 0.0f;
+        far = SIGMOID && __any(s.top > 40.0f);
     }
+    if (a.counts) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dot = fmaf(SIGMOID ? r[i] : e[i], f[i], dot);
+        dot = lanes_sum<L>(dot) * s.rinv;
+        b *= s.rinv;
+        zs *= s.lse * s.inv;
+    }
+
+    // the weights' part: each pair's own term, and the pull on every logit
+    float term[KP];
     if (a.dw) {
-        const int id = lane < a.k ? a.ids[(size_t)t * a.k + lane] : -1;
-        const bool valid = id >= 0 && id < E;
-        const float dw = valid ? a.scale * a.dw[(size_t)t * a.k + lane] : 0.0f, z = valid ? row[id] : -INFINITY;
-        float term = 0.0f;  // the pair's own
-        if (SIGMOID && !a.renormalize) {
-            term = valid ? sigmoid_f32(z) * sigmoid_f32(-z) * dw : 0.0f;
-        } else if (a.renormalize) {
-            const float m = wave_max(z);
-            float u = exp_f32(z - (m == -INFINITY ? 0.0f : m));
-            if (SIGMOID) u = m < 0.0f ? u * sigmoid_f32(-z) : sigmoid_f32(z);
-            const float sum = wave_sum(u);
-            u = sum == 0.0f ? 0.0f : u / sum;
-            const float dot = wave_sum(valid ? u * dw : 0.0f);
-            term = valid ? u * (dw - dot) : 0.0f;
-            if (SIGMOID) term = valid ? term * sigmoid_f32(-z) : 0.0f;
-        } else {
-            // softmax over all logits: the weights' sum pulls on every logit
-            const float u = valid ? exp_f32(z - top) * inv : 0.0f;
-            const float dot = wave_sum(valid ? u * dw : 0.0f);
-            term = valid ? u * dw : 0.0f;
+        float u[KP], sum = 0.0f, mean = 0.0f, m = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < R::N; ++i) d[i] = -soft[i] * dot;
+        for (int i = 0; i < KP; ++i) m = fmaxf(m, z[i]);
+        if (a.renormalize) m = lanes_max<L>(m);
+        const float top = a.renormalize ? (m == -INFINITY ? 0.0f : m) : s.top;
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            if (SIGMOID) u[i] = a.renormalize && m < 0.0f ? exp_down(z[i] - top) * sigmoid_f32(-z[i]) : sigmoid_f32(z[i]);
+            else u[i] = exp_down(z[i] - top);
+            sum += u[i];
         }
-        for (int j = 0; j < a.k; ++j) {
-            const int at = __builtin_amdgcn_readlane(id, j);
-            const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(term), j));
-            if (at < 0 || at >= E) continue;
-            const int unit = at / VEC, reg = unit / 64 * VEC + at % VEC;
+        if (a.renormalize) sum = lanes_sum<L>(sum);
 #pragma unroll
-            for (int i = 0; i < R::N; ++i)
-                if (i == reg) d[i] += lane == unit % 64 ? v : 0.0f;
+        for (int i = 0; i < KP; ++i) {
+            // divided: the weight of a single expert is 1 exactly, its gradient 0
+            if (a.renormalize) u[i] = sum == 0.0f ? 0.0f : u[i] / sum;
+            else if (!SIGMOID) u[i] *= s.inv;
+            if (!valid[i]) u[i] = 0.0f;
+            mean += valid[i] ? u[i] * dw[i] : 0.0f;
+        }
+        mean = a.renormalize || !SIGMOID ? lanes_sum<L>(mean) : 0.0f;
+        if (!a.renormalize) {
+            draw = mean * s.inv;  // of every logit (0 for SIGMOID)
+            mean = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            term[i] = valid[i] ? u[i] * (dw[i] - mean) : 0.0f;
+            if (SIGMOID) term[i] = valid[i] ? term[i] * sigmoid_f32(-z[i]) : 0.0f;
         }
     }
-    if (seq >= 0) {
-        const float n = (float)rows_of_all(a.seqs), ng = (float)slot_range(a.seqs, seq).y;
-        const float b = a.dlosses[0] * ((float)E / ((float)a.k * n)) / ng, zs = a.dlosses[1] * (2.0f / n) * lse;
-        const int32_t* counts = a.counts + (size_t)seq * E;
-        float f[R::N], dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < R::N; ++i) {
-            const int e = R::element(i, lane);
-            f[i] = e < E ? b * (float)counts[e] : 0.0f;
-            dot = fmaf(p[i], f[i], dot);
-        }
-        dot = wave_sum(dot);
-#pragma unroll
-        for (int i = 0; i < R::N; ++i) {
-            float v = p[i] * (f[i] - dot);
-            if (SIGMOID) v *= sigmoid_f32(-l[i]);
-            d[i] += v + zs * soft[i];
-        }
-    }
+
     typedef typename DType<OUT>::type T;
     T* out = static_cast<T*>(a.dlogits) + (size_t)t * E;
+    // the part that all logits have
+    auto common = [&](float e, float r, float q, float f) {
+        float d = pull ? -e * draw : 0.0f;
+        if (seq >= 0) d += fmaf(r * b, (f - dot) * q, zs * e);
+        return d;
+    };
 #pragma unroll
-    for (int g = 0; g < NV; ++g) {
-        const int e = R::element(g * VEC, lane);
-        if (e >= E) continue;
-        if constexpr (VEC == 4) {
-            typedef T t4 __attribute__((ext_vector_type(4)));
-            t4 v;
+    for (int g = 0; g < R::NV; ++g) {
+        const int at = R::element(g * R::VEC, lane);
+        typedef T vec __attribute__((ext_vector_type(R::VEC)));
+        vec v;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = (T)d[4 * g + c];
-            *reinterpret_cast<t4*>(out + e) = v;
-        } else {
-            out[e] = (T)d[g];
+        for (int c = 0; c < R::VEC; ++c) {
+            const int i = g * R::VEC + c;
+            v[c] = (T)(whole ? common(e[i], SIGMOID ? r[i] : e[i], SIGMOID ? q[i] : 1.0f, f[i]) : 0.0f);
         }
+        if (live && at < E) *reinterpret_cast<vec*>(out + at) = v;
+    }
+    if (!a.dw) return;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    float all[KP] = {};
+#pragma unroll
+    for (int w = 0; w < KP; ++w)
+        unrolled<L>([&](auto tag) {
+            constexpr int J = decltype(tag)::value;
+            if (w * L + J >= k) return;
+            const int other = lanes_get<L, J>(id[w]);
+            const float v = __int_as_float(lanes_get<L, J>(__float_as_int(term[w])));
+#pragma unroll
+            for (int u = 0; u < KP; ++u) all[u] += other == id[u] ? v : 0.0f;
+        });
+#pragma unroll
+    for (int u = 0; u < KP; ++u) {
+        float d = all[u];
+        if (whole) {
+            const float ez = exp_down(z[u] - s.top), count = a.counts && valid[u] ? (float)counts[id[u]] : 0.0f;
+            float qz;
+            const float rz = score_of<SIGMOID>(z[u], ez, em, far, s.m, qz);
+            d += common(ez, rz, qz, count);
+        }
+        if (live && valid[u]) out[id[u]] = (T)d;
     }
 }
 
-template <int VEC, int NV>
+template <typename R, int KP>
 static void launch_route_grad(const RouterArgs& a, hipStream_t s) {
-    const dim3 grid((a.T + 3) / 4);
+    const dim3 grid((a.T + 4 * R::ROWS - 1) / (4 * R::ROWS));
     auto go = [&](auto sig, auto out) {
-        route_grad_kernel<VEC, NV, decltype(sig)::value, decltype(out)::value><<<grid, 256, 0, s>>>(a);
+        route_grad_kernel<R, KP, decltype(sig)::value, decltype(out)::value><<<grid, 256, 0, s>>>(a);
     };
     auto type = [&](auto sig) {
         if (a.out_dtype == MOE_F32) go(sig, std::integral_constant<int, MOE_F32>{});
@@ -394,8 +492,14 @@ static void launch_route_grad(const RouterArgs& a, hipStream_t s) {
 
 hipError_t launch_route_backward(const RouterArgs& a, hipStream_t s) {
     if (a.T == 0) return hipSuccess;
-    const bool wide = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits);
-    by_width(a.E, wide, [&](auto vec, auto nv) { launch_route_grad<decltype(vec)::value, decltype(nv)::value>(a, s); });
+    const bool wide = a.E % 4 == 0 && aligned16(a.logits) && aligned16(a.dlogits) && aligned16(a.counts);
+    by_width(a.E, wide, [&](auto row) {
+        typedef decltype(row) R;
+        if constexpr (R::L == 16) {
+            if (a.k > 16) return launch_route_grad<R, 4>(a, s);
+        }
+        launch_route_grad<R, 1>(a, s);
+    });
     return hipGetLastError();
 }
 

@@ -84,11 +84,52 @@ __device__ __forceinline__ float exp_f32(float x) {
     return e > 0.0f && e < 3.0e38f ? fmaf(e, 0.6931471805599453f * rest, e) : e;
 }
 
-// Largest value of the wave, in every lane (NaN is passed over).
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+// e^x for x <= 0 (or NaN).
+__device__ __forceinline__ float exp_down(float x) {
+    x = x < -104.0f ? -104.0f : x;  // e^-104 is 0 in fp32
+    const float t = 1.4426950408889634f * x;
+    const float rest = fmaf(1.925963033500e-8f, x, fmaf(1.4426950408889634f, x, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, 0.6931471805599453f * rest, e);
+}
+
+// max(v, the value DPP_CTRL moves into this lane); lanes that get none keep v.  NaN is passed over.
+template <int DPP_CTRL, int ROW_MASK = 0xF>
+__device__ __forceinline__ float dpp_max(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), DPP_CTRL, ROW_MASK,
+                                                               0xF, false)));
+}
+
+// Largest value and sum over each group of L = 16 or 64 lanes, in all of them.
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+    v = dpp_max<0xB1>(v);
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    v = dpp_max<0x140>(v);
+    if (L == 16) return v;
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return L == 16 ? row16_sum(v) : wave_sum(v);
+}
+
+// Value of lane J of each group of L lanes (J < L).
+template <int L, int J>
+__device__ __forceinline__ int lanes_get(int v) {
+    if constexpr (L == 16) return __builtin_amdgcn_update_dpp(0, v, 0x150 + J, 0xF, 0xF, false);  // row_newbcast
+    else return __builtin_amdgcn_readlane(v, J);
+}
+
+// Sum over the four groups of 16 lanes, lane by lane, in all of them.
+__device__ __forceinline__ float sum_of_rows(float v) {
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
 // Part `index` of the slots' rows, cut into parts of `per` rows each, slots in
