@@ -115,7 +115,7 @@ hipError_t launch_combine_backward(const CombineGradArgs& a, hipStream_t s) {
     // them and their gradient (4096 tokens of 8 x 2048: 55.2 us through, 52.3 past), through
     // where it may hold them from before (333 of 6 x 7168: 14.4 and 20.4).
     const size_t bytes = 2 * (size_t)a.T * a.k * a.H * (a.pairs_dtype == MOE_F32 ? 4 : 2);
-    if (bytes > (256u << 20)) launch_pairs<true>(a, threads, s);
+    if (bytes >= (256u << 20)) launch_pairs<true>(a, threads, s);
     else launch_pairs<false>(a, threads, s);
     return hipGetLastError();
 }

@@ -45,18 +45,29 @@ struct RowSums {
     float m, top;     // largest logit; 0 for -inf (a row of nothing)
     float inv, rinv;  // 1 / sum e, 1 / sum r (0 for a row of nothing)
     float lse;
+    float em, rm;     // e^top, and what e / (1 + t) is multiplied by for r
+    bool far;         // e^top, or what e loses below its range, matters: the exponential of each logit
 };
 
-// r of one logit given e, and 1 - s.
+// e of a logit.  The two roundings of its exponent show as |l - top| 2^-24 of e at most.
+__device__ __forceinline__ float exp_from_top(float l, float top) {
+    return __builtin_amdgcn_exp2f(1.4426950408889634f * (l - top));
+}
+
+// r of a logit given e, and q = 1 - s.
 template <bool SIGMOID>
-__device__ __forceinline__ float score_of(float l, float e, float em, bool far, float m, float& q) {
+__device__ __forceinline__ float score_of(const RowSums& s, float l, float e, float& q) {
     if (!SIGMOID) {
         q = 1.0f;
         return e;
     }
-    const float t = far ? exp_f32(l) : e * em;  // far: e^m, or what e lost below e^-104, matters
-    q = __builtin_amdgcn_rcpf(1.0f + t);
-    return m < 0.0f ? e * q : t > 1.0f ? 1.0f - q : t * q;
+    if (s.far) {
+        const float t = exp_f32(l);
+        q = __builtin_amdgcn_rcpf(1.0f + t);
+        return s.m < 0.0f ? e * q : t > 1.0f ? 1.0f - q : t * q;
+    }
+    q = __builtin_amdgcn_rcpf(fmaf(e, s.em, 1.0f));
+    return e * s.rm * q;
 }
 
 // Of a row's logits l: e, r (SIGMOID; else r is e) and q = 1 - s.  Registers behind the row hold -inf.
@@ -68,19 +79,26 @@ __device__ __forceinline__ RowSums probabilities(const float* l, float* e, float
     for (int i = 1; i < R::N; ++i) s.m = fmaxf(s.m, l[i]);
     s.m = lanes_max<R::L>(s.m);
     s.top = s.m == -INFINITY ? 0.0f : s.m;
-    const bool far = SIGMOID && __any(s.top > 40.0f);
-    const float em = SIGMOID ? exp_f32(s.top) : 0.0f;
     float sum = 0.0f, rsum = 0.0f;
 #pragma unroll
     for (int i = 0; i < R::N; ++i) {
-        e[i] = exp_down(l[i] - s.top);
+        e[i] = exp_from_top(l[i], s.top);
         sum += e[i];
     }
     if (SIGMOID) {
+        s.far = __any(s.top > 40.0f);
+        s.em = exp_f32(s.top);
+        s.rm = s.m < 0.0f ? 1.0f : s.em;
+        if (s.far) {
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) {
-            r[i] = score_of<true>(l[i], e[i], em, far, s.m, q[i]);
-            rsum += r[i];
+            for (int i = 0; i < R::N; ++i) rsum += r[i] = score_of<true>(s, l[i], e[i], q[i]);
+        } else {
+            s.far = false;
+#pragma unroll
+            for (int i = 0; i < R::N; ++i) {
+                q[i] = __builtin_amdgcn_rcpf(fmaf(e[i], s.em, 1.0f));
+                rsum += r[i] = e[i] * s.rm * q[i];
+            }
         }
         rsum = lanes_sum<R::L>(rsum);
         s.rinv = rsum == 0.0f ? 0.0f : 1.0f / rsum;
@@ -99,6 +117,7 @@ struct LossParts {  // the workspace: parts of the rows, [parts][E] sums and cou
     float* z;
     float* balance;    // [G * groups of 64 experts]
     int32_t* prefix;   // [G + 1] parts before each sequence
+    int32_t* done;     // workgroups of the second launch that have ended
 };
 
 // Rows of all sequences and of sequence g.
@@ -132,12 +151,17 @@ __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArg
     const int lane = threadIdx.x % R::L, unit = threadIdx.x / R::L, wave = threadIdx.x >> 6, E = a.E;
     hist[threadIdx.x] = 0;
     int seq, q0, nq;
-    const bool any = find_part<kLossThreads>(a.seqs, ws.per, blockIdx.x, blockIdx.x == 0 && !ALONE ? ws.prefix : nullptr,
-                                             seq, q0, nq);
-    if (!any) {
-        if (!ALONE) return;
-        q0 = nq = 0;
+    if (ALONE) {
+        const int2 r = slot_range(a.seqs, 0);
+        q0 = r.x;
+        nq = r.y;
+    } else {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *ws.done = 0;
+        if (!find_part<kLossThreads>(a.seqs, ws.per, blockIdx.x, blockIdx.x == 0 ? ws.prefix : nullptr, seq, q0, nq)) return;
     }
+    // the first ids, requested ahead of the rows
+    const int32_t* ids = a.ids + (size_t)q0 * a.k;
+    const int early = (int)threadIdx.x < nq * a.k ? ids[threadIdx.x] : -1;
     float acc[R::N] = {}, z = 0.0f;
     for (int r0 = 0; r0 < nq; r0 += kLossWaves * R::ROWS) {
         const int row = r0 + unit;
@@ -145,13 +169,14 @@ __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArg
         float l[R::N], e[R::N], r[R::N], q[R::N];
         R::load(a.logits + (size_t)(q0 + min(row, nq - 1)) * E, E, lane, -INFINITY, l);
         const RowSums s = probabilities<R, SIGMOID>(l, e, r, q);
-        const float inv = live ? s.rinv : 0.0f;
+        const float inv = live ? s.rinv : 0.0f;  // the row behind the last is the last once more
 #pragma unroll
-        for (int i = 0; i < R::N; ++i) acc[i] += live ? (SIGMOID ? r[i] : e[i]) * inv : 0.0f;
+        for (int i = 0; i < R::N; ++i) acc[i] = fmaf(SIGMOID ? r[i] : e[i], inv, acc[i]);
         z = live ? fmaf(s.lse, s.lse, z) : z;
     }
-    const int32_t* ids = a.ids + (size_t)q0 * a.k;
-    for (int i = threadIdx.x; i < nq * a.k; i += kLossThreads) {
+    __syncthreads();  // hist is cleared
+    if (early >= 0 && early < E) atomicAdd(&hist[early], 1);
+    for (int i = threadIdx.x + kLossThreads; i < nq * a.k; i += kLossThreads) {
         const int id = ids[i];
         if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
     }
@@ -186,10 +211,11 @@ __global__ __launch_bounds__(kLossThreads) void loss_rows_kernel(const RouterArg
     }
 }
 
-// Counts and means of 64 experts of a sequence: 64 columns by 16 lanes of parts.
+// Counts and means of 64 experts of a sequence: 64 columns by 16 lanes of parts.  The
+// workgroup that ends last adds the losses' parts, in their order.
 __global__ __launch_bounds__(1024) void loss_join_kernel(const RouterArgs a, const LossParts ws) {
     __shared__ float sp[1024];
-    __shared__ int sc[1024];
+    __shared__ int sc[1024], last;
     const int g = blockIdx.x, e = blockIdx.y * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6, E = a.E;
     const int from = ws.prefix[g], to = min(ws.prefix[g + 1], ws.parts), n = slot_range(a.seqs, g).y;
     float p = 0.0f;
@@ -202,30 +228,36 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(const RouterArgs a, con
     sp[threadIdx.x] = p;
     sc[threadIdx.x] = c;
     __syncthreads();
-    if (lane > 0) return;
-    for (int i = 1; i < 16; ++i) {
-        p += sp[threadIdx.x + 64 * i];
-        c += sc[threadIdx.x + 64 * i];
+    const int groups = gridDim.y, total = gridDim.x * groups;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+            p += sp[threadIdx.x + 64 * i];
+            c += sc[threadIdx.x + 64 * i];
+        }
+        const float mean = n > 0 ? p / (float)n : 0.0f;
+        if (e < E) {
+            a.counts_out[(size_t)g * E + e] = c;
+            a.probs[(size_t)g * E + e] = mean;
+        }
+        const float b = wave_sum(e < E ? (float)c * mean : 0.0f);
+        if (threadIdx.x == 0) {
+            __hip_atomic_store(ws.balance + g * groups + blockIdx.y, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            last = __hip_atomic_fetch_add(ws.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == total - 1;
+        }
     }
-    const float mean = n > 0 ? p / (float)n : 0.0f;
-    if (e < E) {
-        a.counts_out[(size_t)g * E + e] = c;
-        a.probs[(size_t)g * E + e] = mean;
-    }
-    const float b = wave_sum(e < E ? (float)c * mean : 0.0f);
-    if (threadIdx.x == 0) ws.balance[g * gridDim.y + blockIdx.y] = b;
-}
-
-__global__ __launch_bounds__(1024) void loss_sum_kernel(const RouterArgs a, const LossParts ws, int groups) {
+    __syncthreads();
+    if (!last) return;
     float b = 0.0f, z = 0.0f;
-    for (int i = threadIdx.x; i < a.seqs.S * groups; i += 1024) b += ws.balance[i];
-    const int parts = min(ws.prefix[a.seqs.S], ws.parts), n = rows_of_all(a.seqs);
+    for (int i = threadIdx.x; i < total; i += 1024)
+        b += __hip_atomic_load(ws.balance + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int parts = min(ws.prefix[a.seqs.S], ws.parts), rows = rows_of_all(a.seqs);
     for (int i = threadIdx.x; i < parts; i += 1024) z += ws.z[i];
     b = group_sum<16>(b);
     z = group_sum<16>(z);
     if (threadIdx.x == 0) {
-        a.losses[0] = n > 0 ? b * ((float)a.E / ((float)a.k * (float)n)) : 0.0f;
-        a.losses[1] = n > 0 ? z / (float)n : 0.0f;
+        a.losses[0] = rows > 0 ? b * ((float)E / ((float)a.k * (float)rows)) : 0.0f;
+        a.losses[1] = rows > 0 ? z / (float)rows : 0.0f;
     }
 }
 
@@ -252,6 +284,7 @@ static LossParts loss_parts(int T, int E, int G, void* ws, size_t* bytes) {
     l.z = static_cast<float*>(take(l.parts));
     l.balance = static_cast<float*>(take(G * groups));
     l.prefix = static_cast<int32_t*>(take(G + 1));
+    l.done = static_cast<int32_t*>(take(1));
     if (bytes) *bytes = at;
     return l;
 }
@@ -297,10 +330,7 @@ hipError_t launch_balance_loss(const RouterArgs& a, hipStream_t s) {
     const LossParts ws = loss_parts(a.T, a.E, G, a.ws, nullptr);
     const bool alone = G == 1 && a.T <= ws.per;
     by_width(a.E, a.E % 4 == 0 && aligned16(a.logits), [&](auto row) { launch_loss_rows<decltype(row)>(a, ws, alone, s); });
-    if (!alone) {
-        loss_join_kernel<<<dim3(G, groups), 1024, 0, s>>>(a, ws);
-        loss_sum_kernel<<<1, 1024, 0, s>>>(a, ws, groups);
-    }
+    if (!alone) loss_join_kernel<<<dim3(G, groups), 1024, 0, s>>>(a, ws);
     return hipGetLastError();
 }
 
@@ -366,7 +396,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouterArgs a) {
     float l[N], e[N], r[N], q[N], f[N];
     RowSums s = {};
     int seq = -1;
-    float b = 0.0f, zs = 0.0f, em = 0.0f, dot = 0.0f, draw = 0.0f;
+    float b = 0.0f, zs = 0.0f, dot = 0.0f, draw = 0.0f;
     const int32_t* counts = a.counts;
     if (whole) R::load(row, E, lane, -INFINITY, l);
     if (a.counts) {
@@ -380,12 +410,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouterArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) f[i] = (float)c[i];
     }
-    bool far = false;
-    if (whole) {
-        s = probabilities<R, SIGMOID>(l, e, r, q);
-        em = SIGMOID ? exp_f32(s.top) : 0.0f;
-        far = SIGMOID && __any(s.top > 40.0f);
-    }
+    if (whole) s = probabilities<R, SIGMOID>(l, e, r, q);
     if (a.counts) {
 #pragma unroll
         for (int i = 0; i < N; ++i) dot = fmaf(SIGMOID ? r[i] : e[i], f[i], dot);
@@ -466,9 +491,9 @@ __global__ __launch_bounds__(256) void route_grad_kernel(const RouterArgs a) {
     for (int u = 0; u < KP; ++u) {
         float d = all[u];
         if (whole) {
-            const float ez = exp_down(z[u] - s.top), count = a.counts && valid[u] ? (float)counts[id[u]] : 0.0f;
+            const float ez = exp_from_top(z[u], s.top), count = a.counts && valid[u] ? (float)counts[id[u]] : 0.0f;
             float qz;
-            const float rz = score_of<SIGMOID>(z[u], ez, em, far, s.m, qz);
+            const float rz = score_of<SIGMOID>(s, z[u], ez, qz);
             d += common(ez, rz, qz, count);
         }
         if (live && valid[u]) out[id[u]] = (T)d;

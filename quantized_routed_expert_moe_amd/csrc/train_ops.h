@@ -142,6 +142,13 @@ __device__ __forceinline__ bool find_part(const RowMap& m, int per, int index, i
     __shared__ int wsum[THREADS / 64], found[3];
     constexpr int PER = 1024 / THREADS;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    if (!m.offsets) {
+        slot = 0;
+        q0 = index * per;
+        nq = min(per, m.R - q0);
+        if (prefix && t < 2) prefix[t] = t * ((m.R + per - 1) / per);
+        return nq > 0;
+    }
     int2 r[PER];
     int parts = 0;
 #pragma unroll
