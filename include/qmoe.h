@@ -677,7 +677,7 @@ moe_status moe_expert_act_backward(const void* dy, const void* z, int dtype, int
  * With sequences of one length losses[0] is the mean of their balance losses
  * sum_e f_e P_e with f_e = E counts_e / (k n_g); it is 1 where all is even.
  *
- * logits     device, fp32 [T, E].  A logit of -inf has probability 0; a row of
+ * logits     device, fp32 [T, E], finite or -inf.  A logit of -inf has probability 0; a row of
  *            nothing else has all probabilities 0 and adds nothing to losses[1].
  * topk_ids   device, int32 [T, k]; ids outside [0, E) are not counted.
  * T, E, k    as for moe_route_topk; T up to 2^24 / k.
@@ -735,7 +735,7 @@ moe_status moe_combine_backward(const void* dy, int dy_dtype, const void* y_pair
  *         = |scale| * largest magnitude      (MOE_NORM_MAX; NaN if any is)
  *   outs[i] = grads[i] * scale * min(1, max_norm / (total + eps))
  * scale undoes a loss scale.  A total of infinity gives a factor of 0, one of
- * NaN a factor of NaN.
+ * NaN a factor of NaN; where total + eps is 0 nothing is clipped.
  *
  * grads, counts, dtypes  host arrays of n: device addresses (aligned to their
  *            elements, any more is not needed), elements (0..2^40; NULL may stand for 0),

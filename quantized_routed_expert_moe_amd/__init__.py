@@ -759,8 +759,8 @@ def moe_expert_act_backward(dy, z, slot_offsets, dz, dbias, perm_pair=None, rows
     MOE_ACT_NONE z, dz and h are None and dbias sums dy; else dbias may be None."""
     dev = _op_device()
     dtype, swiglu = dy.dtype, act == MOE_ACT_SWIGLU
-    if dy.dim() != 2:
-        raise ValueError("dy must be a matrix")
+    if dy.dim() != 2 or (slot_offsets is not None and slot_offsets.dim() != 1):
+        raise ValueError("dy must be a matrix and slot_offsets int32 [S + 1]")
     N = dy.shape[1] * (2 if swiglu else 1)
     S = dbias.shape[0] if dbias is not None and dbias.dim() == 2 else 1 if slot_offsets is None else slot_offsets.shape[0] - 1
     R = _op_rows(slot_offsets, S, perm_pair, dy, (rows,), 1)

@@ -209,7 +209,7 @@ __device__ __forceinline__ void clip_out(const GradTable<kClipList, true>& t, in
 
 __global__ __launch_bounds__(256) void grad_clip_kernel(const GradTable<kClipList, true> t, const float* total,
                                                         float max_norm, float eps, float scale) {
-    const double limit = (double)max_norm / ((double)total[0] + (double)eps);
+    const double norm = (double)total[0] + (double)eps, limit = norm == 0.0 ? 1.0 : (double)max_norm / norm;
     const float factor = (float)((double)scale * (limit > 1.0 ? 1.0 : limit));  // NaN stays
     const uint32_t c = blockIdx.x;
     const int i = tensor_of(t, c);

@@ -133,6 +133,41 @@ def test_infinite_and_nan_sums(kind):
     assert (got[0] == float("inf")).all()
 
 
+def test_more_than_4_gb_of_rows():
+    """Rows and sums behind 2^32 bytes, through both product kernels and the gradient."""
+    R, N, K = (1 << 20) + 77, 2816, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((R, K), generator=g, device="cuda", dtype=BF)
+    w, b = rand((1, N, K), BF, 2, 0.25).cuda(), rand((1, N), F32, 3).cuda()
+    y = torch.empty((R, N // 2), dtype=BF, device="cuda")
+    z = torch.empty((R, N), dtype=BF, device="cuda")
+    Q.moe_expert_gemm_bias(x, w, b, None, None, y, act=SWI, z=z)
+    for rows in (slice(0, 100), slice(R - 200, R)):
+        v = x[rows].double() @ w[0].double().t() + b[0].double()
+        within(z[rows], v.cpu(), 40 * F * (1 + v.abs().cpu()) + store_bound(v.cpu(), BF), "z")
+        o = act(v, SWI).cpu()
+        within(y[rows], o, 40 * F * (1 + v.abs().cpu()).max() ** 2 + store_bound(o, BF), "y")
+    last = torch.full((R,), R - 1, dtype=torch.int32, device="cuda")  # few rows, the last ones of the buffers
+    last[:3] = torch.tensor([R - 1, R - 2, 5], dtype=torch.int32)
+    off = torch.tensor([0] + [3] * 600, dtype=torch.int32, device="cuda")
+    few_w = w.expand(600, N, K)
+    y2 = torch.empty_like(y)
+    Q.moe_expert_gemm_bias(x, few_w.contiguous(), None, y, off, y2, last, 1, PAIR, PAIR, SWI)
+    for r in (R - 1, R - 2, 5):
+        o = act(x[r:r + 1].double() @ w[0].double().t(), SWI) + y[r:r + 1].double()
+        within(y2[r:r + 1], o.cpu(), 40 * F * (1 + o.abs().cpu()) * 8 + store_bound(o.cpu(), BF), "row")
+    del y2, few_w
+    ws = torch.empty(Q.moe_expert_act_backward_workspace_size(1, N, R), dtype=torch.uint8, device="cuda")
+    db = torch.empty((1, N), device="cuda")
+    end = z[R - 50:].clone()
+    Q.moe_expert_act_backward(y, z, None, z, db, act=SWI, ws=ws)
+    want = act_grad(end.cpu().to(D), y[R - 50:].cpu().to(D), SWI)
+    within(z[R - 50:], want, 16 * F * (1 + end.cpu().to(D).abs().max()) ** 3 + store_bound(want, BF), "dz")
+    # the stored dz has one rounding to bf16 each; their sum is the fp32 sum's up to those
+    total, size = z.double().sum(0), z.double().abs().sum(0)
+    assert ((db[0] - total).abs() <= (2.0 ** -8 + sum_terms(R)) * size).all()
+
+
 # --------------------------------------------------------------- gradients
 
 def run_grad(sizes, N, dtype, kind, rows=POS, k=1, P=None, h=True, bias=True, seed=0, inplace=None, dense=False, scale=1.5):

@@ -176,6 +176,15 @@ def test_infinite_and_nan_totals():
     assert torch.isnan(g[0]).all() and torch.isnan(g[1]).all()
 
 
+def test_zero_gradients_stay_zero():
+    g = [torch.zeros(100, device="cuda"), torch.zeros(9, dtype=BF, device="cuda")]
+    total = norm(g)
+    for max_norm, eps in ((1.0, 0.0), (0.0, 0.0), (0.0, 1e-6)):
+        out = [torch.full_like(t, 3.0) for t in g]
+        Q.moe_grad_clip(g, total, max_norm, eps, outs=out)
+        assert float(total) == 0.0 and all((o == 0).all() for o in out)
+
+
 def test_small_norms_leave_the_gradients():
     g = [rand((100,), BF, 1).cuda(), rand((7,), F32, 2).cuda()]
     keep = [t.clone() for t in g]
