@@ -745,20 +745,29 @@ moe_status moe_combine_backward(const void* dy, int dy_dtype, const void* y_pair
  *            (in place, one type) or does not overlap any gradient.  outs = NULL:
  *            all in place.  In place a factor of 1 leaves the memory as it is.
  * No two gradients overlap.  n in 0..2^20.
+ * table, out_table  device, 8-byte aligned: copies of what moe_grad_table (host, synchronous)
+ *            wrote into host memory of moe_grad_table_size(n) bytes for the same grads and
+ *            outs; or NULL.  With them a list of any length takes one launch instead of
+ *            one for each 160 to 240 tensors.  They are read when the call's work
+ *            runs, so they stay until then; a call that is being captured does without.
  * total      device, fp32 [1].  moe_grad_clip reads it: between the two calls the
  *            caller may join it with other ranks' norms.
  * max_norm   >= 0; eps >= 0, finite; scale finite.
  * ws         device workspace of moe_grad_norm_workspace_size(n), 16-byte aligned.
- * Squares are summed in 64 bits in an order fixed by the counts, so that no sum
- * overflows; the factor is taken in 64 bits and rounded to fp32, and each output
+ * Squares are summed in 64 bits in an order fixed by the counts (and by whether a table
+ * is used), so that no sum overflows; the factor is taken in 64 bits and rounded to fp32, and each output
  * once more.
  */
+size_t moe_grad_table_size(int n);
+moe_status moe_grad_table(const void* const* at, const int64_t* counts, const int32_t* dtypes, int n, void* table,
+                          size_t table_bytes);
 size_t moe_grad_norm_workspace_size(int n);
-moe_status moe_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n, int kind,
-                         float scale, float* total, void* ws, size_t ws_bytes, void* stream);
-moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, void* const* outs,
-                         const int32_t* out_dtypes, int n, const float* total, float max_norm, float eps, float scale,
+moe_status moe_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n,
+                         const void* table, int kind, float scale, float* total, void* ws, size_t ws_bytes,
                          void* stream);
+moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n,
+                         const void* table, void* const* outs, const int32_t* out_dtypes, const void* out_table,
+                         const float* total, float max_norm, float eps, float scale, void* stream);
 
 /* ------------------------------------------------------------ stage timers
  * Diagnostics: one hipEvent pair per launch of a stage, attached to the

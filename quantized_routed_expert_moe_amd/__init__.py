@@ -112,8 +112,11 @@ def lib() -> ctypes.CDLL:
         L.moe_combine_backward.argtypes = [vp, i32, vp, i32, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp]
         L.moe_grad_norm_workspace_size.argtypes = [i32]
         L.moe_grad_norm_workspace_size.restype = sz
-        L.moe_grad_norm.argtypes = [vp, vp, vp, i32, i32, f32, vp, vp, sz, vp]
-        L.moe_grad_clip.argtypes = [vp, vp, vp, vp, vp, i32, vp, f32, f32, f32, vp]
+        L.moe_grad_table_size.argtypes = [i32]
+        L.moe_grad_table_size.restype = sz
+        L.moe_grad_table.argtypes = [vp, vp, vp, i32, vp, sz]
+        L.moe_grad_norm.argtypes = [vp, vp, vp, i32, vp, i32, f32, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, vp, f32, f32, f32, vp]
         for name in ("moe_route_topk", "moe_build_expert_batches", "moe_route_and_batch", "moe_count_routes",
                      "moe_pack_expert", "moe_unpack_expert", "moe_pack_q4k", "moe_pack_q8_0",
                      "moe_validate_slot_map", "moe_expert_ffn_q4k", "moe_expert_ffn_q8_0", "moe_expert_ffn_mxfp4",
@@ -123,7 +126,7 @@ def lib() -> ctypes.CDLL:
                      "moe_prefill_inner_probe", "moe_expert_gemm", "moe_expert_gemm_wgrad", "moe_expert_gemv_w4",
                      "moe_block_norm", "moe_block_norm_backward", "moe_swiglu", "moe_swiglu_backward",
                      "moe_expert_gemm_bias", "moe_expert_act_backward", "moe_balance_loss", "moe_route_backward",
-                     "moe_combine_backward", "moe_grad_norm", "moe_grad_clip"):
+                     "moe_combine_backward", "moe_grad_table", "moe_grad_norm", "moe_grad_clip"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -861,9 +864,10 @@ def moe_combine_backward(dy, y_pairs, topk_ids, topk_w, slot_of_expert, S: int, 
 
 # ------------------------------------------- gradient norm and clipping
 
-class moe_tensor_list:
-    """Tensors as the list calls take them: checked once, their storages kept alive.  A program whose gradients stay
-    where they are builds it once; the calls also take a plain list and build it each time."""
+class _TensorList:
+    """Tensors as the list calls take them: checked once, their storages kept alive."""
+
+    table = stream = None
 
     def __init__(self, tensors):
         self.device = _op_device()
@@ -889,9 +893,26 @@ class moe_tensor_list:
     def __len__(self) -> int:
         return self.n
 
+    def table_on(self, stream: int) -> int:
+        """The table's address for a call on the stream that it was copied on (its memory is that stream's), else 0."""
+        return self.table.data_ptr() if self.table is not None and stream == self.stream else 0
 
-def _op_list(tensors, device: int) -> moe_tensor_list:
-    lst = tensors if type(tensors) is moe_tensor_list else moe_tensor_list(tensors)
+
+class moe_tensor_list(_TensorList):
+    """A list of tensors for moe_grad_norm and moe_grad_clip, which also take a plain list and build one each time.  A
+    program whose gradients stay where they are builds it once and keeps it.  Its table is copied to the device, on the
+    current stream, unless that is being captured."""
+
+    def __init__(self, tensors):
+        super().__init__(tensors)
+        if self.n and not _torch.cuda.is_current_stream_capturing():
+            host = _torch.empty(lib().moe_grad_table_size(self.n), dtype=_U8)
+            _check(lib().moe_grad_table(self.c_at, self.c_counts, self.c_codes, self.n, host.data_ptr(), host.numel()))
+            self.table, self.stream = host.to(f"cuda:{self.device}"), _raw_stream(self.device)
+
+
+def _op_list(tensors, device: int) -> _TensorList:
+    lst = tensors if type(tensors) is moe_tensor_list else _TensorList(tensors)
     if lst.device != device:
         raise TypeError(f"the list's tensors must be on the current device (cuda:{device})")
     return lst
@@ -915,8 +936,9 @@ def moe_grad_norm(grads, total, kind: int = MOE_NORM_L2, scale: float = 1.0, ws=
     lst = _op_list(grads, dev)
     _op_total(total)
     tp, sp = _op_ptrs(dev, "total ws", total, ws)
-    _check(lib().moe_grad_norm(lst.c_at, lst.c_counts, lst.c_codes, lst.n, kind, float(scale), tp, sp,
-                               0 if ws is None else ws.numel() * ws.element_size(), _op_stream(dev, stream)))
+    stream = _op_stream(dev, stream)
+    _check(lib().moe_grad_norm(lst.c_at, lst.c_counts, lst.c_codes, lst.n, lst.table_on(stream), kind, float(scale), tp,
+                               sp, 0 if ws is None else ws.numel() * ws.element_size(), stream))
 
 
 def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float = 1.0, outs=None, stream=None):
@@ -925,17 +947,18 @@ def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float
     lst = _op_list(grads, dev)
     _op_total(total)
     tp, = _op_ptrs(dev, "total", total)
-    op = oc = None
+    stream = _op_stream(dev, stream)
+    op = oc = ot = None
     if outs is not None:
         out = _op_list(outs, dev)
         if lst.apart is not out:
             _op_apart(lst, out)
-        op, oc = out.c_at, out.c_codes
-    _check(lib().moe_grad_clip(lst.c_at, lst.c_counts, lst.c_codes, op, oc, lst.n, tp, float(max_norm), float(eps),
-                               float(scale), _op_stream(dev, stream)))
+        op, oc, ot = out.c_at, out.c_codes, out.table_on(stream)
+    _check(lib().moe_grad_clip(lst.c_at, lst.c_counts, lst.c_codes, lst.n, lst.table_on(stream), op, oc, ot, tp,
+                               float(max_norm), float(eps), float(scale), stream))
 
 
-def _op_apart(lst: moe_tensor_list, out: moe_tensor_list) -> None:
+def _op_apart(lst: _TensorList, out: _TensorList) -> None:
     """Every output is its own gradient or overlaps none.  Lists do not change, so a pair of them is looked at once."""
     if out.counts != lst.counts:
         raise ValueError("outs must have the sizes of grads")

@@ -24,6 +24,7 @@ moe_status launched(hipError_t e, const char* what) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool half_type(int t) { return t == MOE_BF16 || t == MOE_F16; }
 bool any_type(int t) { return t == MOE_F32 || half_type(t); }
 
@@ -408,23 +409,39 @@ static moe_status check_list(const void* const* at, const int64_t* counts, const
 
 size_t moe_grad_norm_workspace_size(int n) { return n < 0 || n > (1 << 20) ? 0 : qmoe::grad_norm_workspace_bytes(n); }
 
-moe_status moe_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n, int kind,
-                         float scale, float* total, void* ws, size_t ws_bytes, void* stream) {
+size_t moe_grad_table_size(int n) { return n < 0 || n > (1 << 20) ? 0 : qmoe::grad_table_bytes(n); }
+
+moe_status moe_grad_table(const void* const* at, const int64_t* counts, const int32_t* dtypes, int n, void* table,
+                          size_t table_bytes) {
+    moe_status st = check_list(at, counts, dtypes, n, "at");
+    if (st != MOE_OK) return st;
+    if (n > 0 && !table) return fail(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (table_bytes < qmoe::grad_table_bytes(n))
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "table %zu bytes, %zu needed", table_bytes, qmoe::grad_table_bytes(n));
+    qmoe::fill_grad_table(at, counts, dtypes, n, table);
+    return MOE_OK;
+}
+
+moe_status moe_grad_norm(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n,
+                         const void* table, int kind, float scale, float* total, void* ws, size_t ws_bytes,
+                         void* stream) {
     moe_status st = check_list(grads, counts, dtypes, n, "grads");
     if (st != MOE_OK) return st;
     if (kind != MOE_NORM_L2 && kind != MOE_NORM_MAX) return fail(MOE_ERR_INVALID_ARGUMENT, "bad norm kind %d", kind);
     if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARGUMENT, "scale must be finite");
     if (!total) return fail(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (!aligned8(table)) return fail(MOE_ERR_INVALID_ARGUMENT, "a table must be 8-byte aligned");
     const size_t need = qmoe::grad_norm_workspace_bytes(n);
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", ws_bytes, need);
     if (!ws || !aligned16(ws)) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be non-NULL and 16-byte aligned");
-    const qmoe::GradListArgs a{grads, counts, dtypes, nullptr, nullptr, n, kind, scale, 0.0f, 0.0f, total, ws};
+    const qmoe::GradListArgs a{grads, counts, dtypes, nullptr, nullptr, n, kind, scale, 0.0f, 0.0f, total, ws,
+                               table, nullptr};
     return launched(qmoe::launch_grad_norm(a, (hipStream_t)stream), "gradient norm launch");
 }
 
-moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, void* const* outs,
-                         const int32_t* out_dtypes, int n, const float* total, float max_norm, float eps, float scale,
-                         void* stream) {
+moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const int32_t* dtypes, int n,
+                         const void* table, void* const* outs, const int32_t* out_dtypes, const void* out_table,
+                         const float* total, float max_norm, float eps, float scale, void* stream) {
     moe_status st = check_list(grads, counts, dtypes, n, "grads");
     if (st != MOE_OK) return st;
     if ((outs != nullptr) != (out_dtypes != nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "outs and out_dtypes go together");
@@ -433,10 +450,12 @@ moe_status moe_grad_clip(const void* const* grads, const int64_t* counts, const 
         if (counts[i] > 0 && outs[i] == grads[i] && out_dtypes[i] != dtypes[i])
             return fail(MOE_ERR_INVALID_ARGUMENT, "outs[%d] is grads[%d] in another type", i, i);
     if (!total) return fail(MOE_ERR_INVALID_ARGUMENT, "a required pointer is NULL");
+    if (!aligned8(table) || !aligned8(out_table)) return fail(MOE_ERR_INVALID_ARGUMENT, "a table must be 8-byte aligned");
     if (!(max_norm >= 0.0f)) return fail(MOE_ERR_INVALID_ARGUMENT, "max_norm must be >= 0");
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MOE_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
     if (!std::isfinite(scale)) return fail(MOE_ERR_INVALID_ARGUMENT, "scale must be finite");
-    const qmoe::GradListArgs a{grads, counts, dtypes, outs, out_dtypes, n, 0, scale, max_norm, eps, const_cast<float*>(total), nullptr};
+    const qmoe::GradListArgs a{grads, counts, dtypes, outs, out_dtypes, n, 0, scale, max_norm, eps, const_cast<float*>(total),
+                               nullptr, table, out_table};
     return launched(qmoe::launch_grad_clip(a, (hipStream_t)stream), "gradient clipping launch");
 }
 

@@ -68,7 +68,11 @@ struct GradListArgs {
     float scale, max_norm, eps;
     float* total;
     void* ws;
+    const void* table;  // on the device, or NULL
+    const void* out_table;
 };
+size_t grad_table_bytes(int n);
+void fill_grad_table(const void* const* at, const int64_t* counts, const int32_t* dtypes, int n, void* table);
 size_t grad_norm_workspace_bytes(int n);
 hipError_t launch_grad_norm(const GradListArgs& a, hipStream_t s);
 hipError_t launch_grad_clip(const GradListArgs& a, hipStream_t s);

@@ -69,6 +69,66 @@ def test_long_lists(n):
     check(sizes, [(BF, HF, F32)[i % 3] for i in range(n)], None, 1.5)
 
 
+@pytest.mark.parametrize("n", [161, 241, 317, 4100])
+@pytest.mark.parametrize("out", [None, BF])
+def test_long_lists_by_their_table(n, out):
+    """A kept list of more tensors than a launch's arguments hold: one launch, the results of the plain list."""
+    sizes = [0 if i % 50 == 7 else 1 + (i * 37) % 300 for i in range(n)]
+    sizes[n // 2] = 70001
+    types = [(BF, HF, F32)[i % 3] for i in range(n)]
+    grads = [rand((s,), t, i).cuda() for i, (s, t) in enumerate(zip(sizes, types))]
+    plain = [g.clone() for g in grads]
+    lst, want = Q.moe_tensor_list(grads), exact(grads)
+    assert lst.table is not None
+    for kind, w in ((Q.MOE_NORM_L2, want), (Q.MOE_NORM_MAX, exact(grads, Q.MOE_NORM_MAX))):
+        assert abs(float(norm(lst, kind)) - w) <= F * w * 1.001
+    total = norm(lst)
+    make = lambda: None if out is None else [torch.full((s,), -7.0, dtype=out, device="cuda") for s in sizes]
+    a, b = make(), make()
+    Q.moe_grad_clip(plain, total, 3.0, outs=a)
+    kept = None if b is None else Q.moe_tensor_list(b)
+    Q.moe_grad_clip(lst, total, 3.0, outs=kept)
+    for p, q in zip(a or plain, b or grads):
+        assert torch.equal(p, q)
+    s = torch.cuda.Stream()  # another stream than the table's: the arguments carry the list
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        assert lst.table_on(torch.cuda.current_stream().cuda_stream) == 0
+        again = norm(lst)
+    s.synchronize()
+    w = exact(grads)
+    assert abs(float(again) - w) <= F * w * 1.001
+
+
+def test_long_list_captured_outlives_its_table():
+    grads = [rand((100 + i,), F32, i).cuda() for i in range(300)]
+    total, ws = torch.zeros(1, device="cuda"), torch.empty(Q.moe_grad_norm_workspace_size(300), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(g) for g in grads]
+    lst, out = Q.moe_tensor_list(grads), Q.moe_tensor_list(outs)
+    Q.moe_grad_norm(lst, total, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.moe_grad_norm(lst, total, ws=ws)
+        Q.moe_grad_clip(lst, total, 2.0, outs=out)
+        inside = Q.moe_tensor_list(grads)  # no copy while capturing
+        assert inside.table is None
+        Q.moe_grad_norm(inside, total, ws=ws)
+    del lst, out, inside
+    fill = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")  # what the tables' memory may hold by now
+    for seed in range(3):
+        for g in grads:
+            g.copy_(rand(g.shape, F32, seed * 1000 + g.numel()))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = exact(grads)
+        assert abs(float(total) - want) <= F * want * 1.001
+        for g, o in zip(grads, outs):
+            w = g.cpu().to(D) * min(1.0, 2.0 / (want + 1e-6))
+            within(o, w, 3 * F * w.abs() * 1.001, "clipped")
+    assert int(fill[0]) == 255
+
+
 def test_empty_lists_and_tensors():
     assert float(norm([])) == 0.0
     empty = [torch.empty(0, dtype=BF, device="cuda"), torch.empty((0, 5), device="cuda")]

@@ -154,14 +154,15 @@ def _list(values, ctype):
     return None if values is None else (ctype * len(values))(*values)
 
 
-def _norm(at=(FAKE,), counts=(8,), types=(0,), n=None, kind=0, scale=1.0, total=FAKE, ws=FAKE, wsb=1 << 40):
+def _norm(at=(FAKE,), counts=(8,), types=(0,), n=None, table=None, kind=0, scale=1.0, total=FAKE, ws=FAKE, wsb=1 << 40):
     return _call("moe_grad_norm", _list(at, ctypes.c_void_p), _list(counts, ctypes.c_int64), _list(types, ctypes.c_int32),
-                 len(at) if n is None else n, kind, f32(scale), total, ws, wsb, None)
+                 len(at) if n is None else n, table, kind, f32(scale), total, ws, wsb, None)
 
 
-def _clip(at=(FAKE,), counts=(8,), types=(0,), outs=None, otypes=None, n=None, total=FAKE, max_norm=1.0, eps=1e-6, scale=1.0):
+def _clip(at=(FAKE,), counts=(8,), types=(0,), n=None, table=None, outs=None, otypes=None, otable=None, total=FAKE, max_norm=1.0,
+          eps=1e-6, scale=1.0):
     return _call("moe_grad_clip", _list(at, ctypes.c_void_p), _list(counts, ctypes.c_int64), _list(types, ctypes.c_int32),
-                 _list(outs, ctypes.c_void_p), _list(otypes, ctypes.c_int32), len(at) if n is None else n, total,
+                 len(at) if n is None else n, table, _list(outs, ctypes.c_void_p), _list(otypes, ctypes.c_int32), otable, total,
                  f32(max_norm), f32(eps), f32(scale), None)
 
 
@@ -171,7 +172,7 @@ def _clip(at=(FAKE,), counts=(8,), types=(0,), outs=None, otypes=None, n=None, t
     (dict(types=None), "NULL"), (dict(types=(3,)), "grads[0]"), (dict(counts=(-1,)), "grads[0]"),
     (dict(counts=((1 << 40) + 1,)), "2^40"), (dict(at=(None,)), "grads[0] is NULL"), (dict(at=(FAKE + 2,)), "aligned"),
     (dict(at=(FAKE, FAKE + 1), counts=(8, 8), types=(0, 1)), "grads[1]"), (dict(total=None), "NULL"),
-    (dict(scale=float("inf")), "scale"),
+    (dict(scale=float("inf")), "scale"), (dict(table=FAKE + 4), "table"),
 ])
 def test_gradient_list_refusals(call, kw, needle):
     _refused(call(**kw), INV, needle)
@@ -189,7 +190,7 @@ def test_gradient_norm_refusals(kw, want, needle):
     (dict(max_norm=-1.0), "max_norm"), (dict(max_norm=float("nan")), "max_norm"), (dict(eps=-1.0), "eps"),
     (dict(eps=float("inf")), "eps"), (dict(outs=(FAKE * 2,)), "go together"), (dict(otypes=(0,)), "go together"),
     (dict(outs=(FAKE * 2,), otypes=(5,)), "outs[0]"), (dict(outs=(FAKE * 2 + 1,), otypes=(0,)), "outs[0]"),
-    (dict(outs=(FAKE,), otypes=(1,)), "another type"),
+    (dict(outs=(FAKE,), otypes=(1,)), "another type"), (dict(otable=FAKE + 2), "table"),
 ])
 def test_gradient_clip_refusals(kw, needle):
     _refused(_clip(**kw), INV, needle)
@@ -198,6 +199,23 @@ def test_gradient_clip_refusals(kw, needle):
 def test_gradient_clip_of_an_empty_list():
     assert _clip(at=(), counts=(), types=(), n=0)[0] == Q.MOE_OK
     assert _clip(at=(None,), counts=(0,), types=(1,))[0] == Q.MOE_OK
+
+
+def test_gradient_table():
+    """Empty tensors are left out; chunks are of 4096 elements while the list is short."""
+    at, counts, types = (FAKE, None, FAKE * 2, FAKE * 3), (5000, 0, 3, 4096), (1, 0, 0, 2)
+    size = Q.lib().moe_grad_table_size(4)
+    assert size == 4 * 24 and Q.lib().moe_grad_table_size(-1) == 0 and Q.lib().moe_grad_table_size((1 << 20) + 1) == 0
+    table = (ctypes.c_uint64 * 12)()
+    args = lambda **kw: [_list(kw.get("at", at), ctypes.c_void_p), _list(kw.get("counts", counts), ctypes.c_int64),
+                         _list(kw.get("types", types), ctypes.c_int32), 4, kw.get("table", table), kw.get("size", size)]
+    assert _call("moe_grad_table", *args())[0] == Q.MOE_OK
+    both = lambda first: first | first << 32
+    assert list(table) == [FAKE, 5000 | 1 << 60, both(0), FAKE * 2, 3, both(2), FAKE * 3, 4096 | 2 << 60, both(3), 0, 0, 0]
+    _refused(_call("moe_grad_table", *args(size=size - 1)), WSS, "needed")
+    _refused(_call("moe_grad_table", *args(table=None)), INV, "NULL")
+    _refused(_call("moe_grad_table", *args(types=(1, 0, 0, 3))), INV, "at[3]")
+    _refused(_call("moe_grad_table", *args(counts=(5000, 0, -3, 1))), INV, "at[2]")
 
 
 def test_gradient_norm_workspace():
