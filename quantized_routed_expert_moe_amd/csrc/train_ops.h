@@ -146,11 +146,12 @@ __device__ __forceinline__ bool find_part(const RowMap& m, int per, int index, i
     __shared__ int wsum[THREADS / 64], found[3];
     constexpr int PER = 1024 / THREADS;
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    if (!m.offsets) {
+    if (m.S == 1) {
+        const int2 r = slot_range(m, 0);
         slot = 0;
-        q0 = index * per;
-        nq = min(per, m.R - q0);
-        if (prefix && t < 2) prefix[t] = t * ((m.R + per - 1) / per);
+        q0 = r.x + index * per;
+        nq = min(per, r.y - index * per);
+        if (prefix && t < 2) prefix[t] = t * ((r.y + per - 1) / per);
         return nq > 0;
     }
     int2 r[PER];
