@@ -41,6 +41,16 @@ __device__ __forceinline__ void act8(int act, float* v) {
     }
 }
 
+// s = 1 / (1 + e^-u) and q = 1 - s, of one exponential (as in sigmoid_f32).
+__device__ __forceinline__ void sigmoid_pair(float u, float& s, float& q) {
+    const float t = -1.4426950408889634f * u;
+    const float rest = fmaf(-1.4426950408889634f, u, -t) - 1.925963033500e-8f * u;
+    const float e0 = __builtin_amdgcn_exp2f(t);
+    const float e = e0 > 0.0f && e0 < 3.0e38f ? fmaf(e0, 0.6931471805599453f * rest, e0) : e0;
+    s = __builtin_amdgcn_rcpf(1.0f + e);
+    q = u < 0.0f ? 1.0f - s : e * s;
+}
+
 // dz = d act'(z), h = act(z).
 __device__ __forceinline__ void act_grad8(int act, const float* z, const float* d, float* dz, float* h) {
     if (act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH) {
@@ -49,7 +59,8 @@ __device__ __forceinline__ void act_grad8(int act, const float* z, const float* 
         for (int i = 0; i < 8; ++i) {
             const float c = act_range(z[i]);
             const float b = silu ? 0.0f : kGeluB, a = silu ? 1.0f : kGeluA;
-            const float u = c * fmaf(b * c, c, a), s = sigmoid_f32(u), q = sigmoid_f32(-u);
+            float s, q;
+            sigmoid_pair(c * fmaf(b * c, c, a), s, q);
             dz[i] = d[i] * (s * fmaf(c * q, fmaf(3.0f * b * c, c, a), 1.0f));
             h[i] = z[i] * s;
         }

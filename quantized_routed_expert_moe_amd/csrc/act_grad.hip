@@ -5,7 +5,7 @@
 // slot and a run of columns; a thread takes eight columns through every rl-th
 // row and holds their sums, which the workgroup joins and stores as one part; a
 // second launch adds a slot's parts in order.  No atomics.  32768 rows of 768 of 128 slots (SwiGLU,
-// h again, bf16): 67 us of inputs from HBM (4.5 TB/s), 58 where the last-level cache holds half of
+// h again, bf16): 66 us of inputs from HBM (4.6 TB/s), 58 where the last-level cache holds half of
 // them, and 4 us for the sums.
 #include "act.h"
 #include "train_ops.h"

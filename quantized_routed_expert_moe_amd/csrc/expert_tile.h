@@ -523,7 +523,9 @@ __device__ __forceinline__ void load8_of(const void* p, int f32, size_t at, floa
 // share of the stage buffers as fp32; a lane takes eight columns of a row, whose bias it holds
 // in registers.  First z and the activation, in place, in a loop that is not unrolled (erf and
 // the rest would be repeated 40 times in the code); then residual, rounding and store, the
-// residual's rows requested before the first part.
+// residual's rows requested before the first part.  With and without operands, us:
+// 32768 pairs of 1536 x 2048 with SwiGLU 253 (bias, z) and 253, by tile_store 274; 2999 rows of
+// 2048 x 4096 64 (bias, residual) and 62, by tile_store 60, with GELU 68.
 template <typename C, int NB>
 __device__ __forceinline__ void tile_store_epilogue(const TileArgs& a, int slot, int q0, int nq, int p0,
                                                     const TileLds<C>& lds, const f32x16 (&acc)[NB][C::PI]) {

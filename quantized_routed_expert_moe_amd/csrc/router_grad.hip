@@ -4,7 +4,8 @@
 // 16 lanes own a row of up to 256 logits, 64 a wider one: it sits in registers, so the
 // largest logit, the sums and the probabilities come out of one read, and a sum over a row is
 // four steps between lanes for four rows at a time (with 64 lanes for every row the gradient of
-// 16384 rows of 256 took 18 us: the vector units' time, not the memory's, which is 5 us).
+// 16384 rows of 256 took 18 us, 10 so: the vector units' time, not the memory's, which is 5 us).
+// Losses of those rows: 8.4 us and 4 for the join.
 // The probabilities' means are sums over rows in registers, joined over a workgroup's
 // waves in LDS, then over workgroups by a second launch in their order: no atomics on
 // floats (the counts' are on integers in LDS).
