@@ -900,8 +900,9 @@ class _TensorList:
 
 class moe_tensor_list(_TensorList):
     """A list of tensors for moe_grad_norm and moe_grad_clip, which also take a plain list and build one each time.  A
-    program whose gradients stay where they are builds it once and keeps it.  Its table is copied to the device, on the
-    current stream, unless that is being captured."""
+    program whose gradients stay where they are builds it once and keeps it: it stands for the memory that the tensors
+    have now, which it keeps alive and which must not be resized.  Its table is copied to the device, on the current
+    stream, unless that is being captured."""
 
     def __init__(self, tensors):
         super().__init__(tensors)

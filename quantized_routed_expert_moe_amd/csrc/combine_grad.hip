@@ -1,8 +1,8 @@
 // The weighted combine's gradients: dy_pairs[p] = w_p dy[t] and dw[p] = <y_pairs[p], dy[t]>.
 //
 // Bound by HBM: each pair's row is read and one written, a token's row of dy read.
-// A workgroup owns a token's pairs, eight at a time: a thread holds eight columns of
-// dy and takes them through the eight pairs, whose loads are in flight together; the
+// A workgroup owns eight of a token's pairs: a thread holds eight columns of
+// dy and takes them through the pairs, whose loads are in flight together; the
 // eight sums are joined in wave order at the end.  Lane j of each wave looks pair j up, so
 // that a token's ids, weights and slots are two loads in a row and not sixteen.
 // 4096 tokens of 8 pairs of 2048, bf16: 57 us of inputs from HBM (5.0 TB/s), 52 where the
@@ -11,7 +11,7 @@
 
 namespace qmoe {
 
-constexpr int kPairs = 8;  // pairs of a pass
+constexpr int kPairs = 8;  // pairs of a workgroup
 
 // load_vec8 past the caches.
 template <int DT>
@@ -32,9 +32,11 @@ __device__ __forceinline__ void load_vec8_past(const void* base, size_t idx, flo
 template <int DP, int DY, bool PAST>
 __global__ __launch_bounds__(512) void combine_grad_kernel(const CombineGradArgs a) {
     __shared__ float part[8][kPairs];
-    const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const size_t row = (size_t)t * a.H, p0 = (size_t)t * a.k;
-    for (int b = 0; b < a.k; b += kPairs) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int passes = (a.k + kPairs - 1) / kPairs;
+    for (int unit = blockIdx.x; unit < a.T * passes; unit += gridDim.x) {
+        const int t = unit / passes, b = unit % passes * kPairs;
+        const size_t row = (size_t)t * a.H, p0 = (size_t)t * a.k;
         const int n = min(kPairs, a.k - b);
         // lane j looks up pair j; all lanes then take it from there
         const int id = a.ids[p0 + b + min(lane, n - 1)];
@@ -94,7 +96,9 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(const CombineGradArgs
 
 template <int DP, bool PAST>
 static void launch_dy(const CombineGradArgs& a, int threads, hipStream_t s) {
-    const dim3 grid(a.T);
+    // up to 2^20 workgroups, which then take several units: a launch's threads stay below 2^32
+    const int units = a.T * ((a.k + kPairs - 1) / kPairs);
+    const dim3 grid(units < (1 << 20) ? units : 1 << 20);
     if (a.dy_dtype == MOE_F32) combine_grad_kernel<DP, MOE_F32, PAST><<<grid, threads, 0, s>>>(a);
     else if (a.dy_dtype == MOE_BF16) combine_grad_kernel<DP, MOE_BF16, PAST><<<grid, threads, 0, s>>>(a);
     else combine_grad_kernel<DP, MOE_F16, PAST><<<grid, threads, 0, s>>>(a);

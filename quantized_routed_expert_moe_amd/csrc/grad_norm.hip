@@ -275,7 +275,7 @@ size_t grad_norm_workspace_bytes(int n) {
 static int chunk_shift(int64_t total, bool clip) {
     int shift = 12;
     while (shift < (clip ? 12 : 14) && (total >> shift) > 2 * kGradBlocks) ++shift;
-    while ((total >> shift) > 1ll << 30) ++shift;
+    while ((total >> shift) > 1ll << 23) ++shift;  // and with them a launch's threads, below 2^32
     return shift;
 }
 static uint32_t chunks_of(int64_t count, int shift) { return (uint32_t)((count + (int64_t(1) << shift) - 1) >> shift); }

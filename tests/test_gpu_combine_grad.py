@@ -127,6 +127,23 @@ def test_many_rows():
         assert ((dw[a:b] - y.sum(2)).abs() <= sum_terms(H) * y.abs().sum(2)).all()
 
 
+@pytest.mark.parametrize("k,H", [(1, 8), (9, 520)])
+def test_more_tokens_than_workgroups(k, H):
+    """2^20 workgroups at most: the others' tokens are taken in turn."""
+    T = (1 << 20) + 777 if k == 1 else 120000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ids = torch.randint(0, 16, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    w, soe = torch.rand((T, k), generator=g, device="cuda"), torch.arange(16, dtype=torch.int32, device="cuda")
+    yp = torch.randn((T * k, H), generator=g, device="cuda", dtype=BF)
+    dy = torch.randn((T, H), generator=g, device="cuda", dtype=BF)
+    dyp, dw = torch.empty_like(yp), torch.empty_like(w)
+    Q.moe_combine_backward(dy, yp, ids, w, soe, 16, dyp, dw)
+    d = dy.float().unsqueeze(1)
+    assert torch.equal(dyp.view(T, k, H), (w.unsqueeze(2) * d).to(BF))
+    y = yp.view(T, k, H).double() * d
+    assert ((dw - y.sum(2)).abs() <= sum_terms(H) * y.abs().sum(2) + 1e-37).all()
+
+
 def test_against_differences_of_the_combine():
     """The combine is linear in the weights and in the pairs: its own differences are the gradients, up to its fp32
     roundings (each of k + 1 sums below 2^-23 of about 8, over 64 columns of |dy| below 5)."""

@@ -218,6 +218,18 @@ def test_gradient_table():
     _refused(_call("moe_grad_table", *args(counts=(5000, 0, -3, 1))), INV, "at[2]")
 
 
+def test_gradient_table_of_the_largest_lists():
+    """The chunks of any list, a workgroup of 256 threads each, stay below 2^32 threads."""
+    n = 4
+    table = (ctypes.c_uint64 * (3 * n))()
+    st, _ = _call("moe_grad_table", _list([FAKE << 20] * n, ctypes.c_void_p), _list([1 << 40] * n, ctypes.c_int64),
+                  _list([1] * n, ctypes.c_int32), n, table, ctypes.sizeof(table))
+    assert st == Q.MOE_OK
+    last = table[3 * n - 1]
+    for first in (last & 0xFFFFFFFF, last >> 32):  # three quarters of the chunks lie before the last tensor
+        assert 0 < first * 4 // 3 * 256 < 1 << 32
+
+
 def test_gradient_norm_workspace():
     size = Q.moe_grad_norm_workspace_size
     assert size(-1) == 0 and size((1 << 20) + 1) == 0 and size(0) > 0 and size(1 << 20) > size(1) > 0
