@@ -14,13 +14,23 @@ namespace qmoe {
 
 constexpr int kRows = 2;  // rows that a thread has in flight
 
-// Rows of a workgroup: 16 and more, so that there are up to 4096 workgroups (32768 rows of
-// 768, SwiGLU: 82 us with 1024, 67 with 2048, 66 with 4096 and 8192; parts of 64 rows take 1001 rows
-// of 2048 from 12 to 15 us).
+// Lanes of eight features that a row of n of them has, as a power of two up to 32.
+static int lane_shift(int n) {
+    int shift = 5;
+    while (shift > 0 && (8 << (shift - 1)) >= n) --shift;
+    return shift;
+}
+
+// Rows of a workgroup: two for each thread, and more for 16384 elements a workgroup while that
+// leaves 512 of them (32768 rows of 768, SwiGLU: 82 us with 1024 workgroups, 67 with 2048, 66 with 4096 and
+// 8192; 1001 rows of 2048 12 us in parts of 16 rows, 15 in 64), and for at most 1024 parts, which the
+// second launch adds (the sums alone of 16384 rows of 128: 23 us with 1024 parts and four columns a
+// lane for 256 of them, 10 so; 2^20 of 64: 96 with 4096 parts, 26 so, 5.2 TB/s).
 static int part_rows(int N, int R) {
-    int per = 16;
-    const long long chunks = (N + 255) / 256;
-    while (per < 4096 && (long long)R / per * chunks > 4096) per *= 2;
+    const long long chunks = (N + 255) / 256, work = (long long)R * N / 16384;
+    const long long most = work < 512 ? 512 : work < 4096 ? work : 4096;
+    int per = 2 * (256 >> lane_shift(N));
+    while (R / per > 1024 || R / per * chunks > most) per *= 2;
     return per;
 }
 static long long part_count(int S, int R, int per) { return (long long)R / per + (S < R ? S : R); }
@@ -99,24 +109,25 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, int 
     }
 }
 
-// dbias_s = the sum of the slot's parts: 256 columns, four a thread, by LANES lanes, whose sums
-// are added in order.
-template <int LANES>
-__global__ __launch_bounds__(64 * LANES) void act_grad_join_kernel(const void* ws, int parts, int N, float* dbias) {
-    __shared__ f32x4 red[64 * LANES];
+// dbias_s = the sum of the slot's parts: up to 256 columns, four a thread, by as many lanes as there
+// are threads left, whose sums are added as a tree.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void act_grad_join_kernel(const void* ws, int parts, int N, int cl_shift, float* dbias) {
+    __shared__ f32x4 red[THREADS];
     const int32_t* prefix = static_cast<const int32_t*>(ws);
-    const int s = blockIdx.x, n = blockIdx.y * 256 + (threadIdx.x & 63) * 4, lane = threadIdx.x >> 6;
+    const int cl = 1 << cl_shift, lanes = THREADS >> cl_shift, lane = threadIdx.x >> cl_shift;
+    const int s = blockIdx.x, n = (blockIdx.y * cl + (threadIdx.x & (cl - 1))) * 4;
     const int from = prefix[s], to = min(prefix[s + 1], parts);
     const float* part = reinterpret_cast<const float*>(static_cast<const uint8_t*>(ws) + 4 * 1028);
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (n < N)
-        for (int p = from + lane; p < to; p += LANES) v += *reinterpret_cast<const f32x4*>(part + (size_t)p * N + n);
+        for (int p = from + lane; p < to; p += lanes) v += *reinterpret_cast<const f32x4*>(part + (size_t)p * N + n);
     red[threadIdx.x] = v;
-    __syncthreads();
-    if (lane > 0 || n >= N) return;
-#pragma unroll
-    for (int i = 1; i < LANES; ++i) v += red[threadIdx.x + 64 * i];
-    *reinterpret_cast<f32x4*>(dbias + (size_t)s * N + n) = v;
+    for (int half = lanes / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (lane < half) red[threadIdx.x] = v += red[threadIdx.x + half * cl];
+    }
+    if (lane == 0 && n < N) *reinterpret_cast<f32x4*>(dbias + (size_t)s * N + n) = v;
 }
 
 // No positions: every sum is zero.
@@ -141,8 +152,7 @@ hipError_t launch_act_grad(const ActGradArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     const int per = part_rows(N, R);
-    int shift = 5;
-    while (shift > 0 && (8 << (shift - 1)) >= I) --shift;
+    const int shift = lane_shift(I);
     const long long parts = part_count(S, R, per), chunks = (I + (8 << shift) - 1) / (8 << shift);
     // The columns of a part side by side: what runs at one time reads whole rows (32768 rows of
     // 768, SwiGLU, inputs from HBM: 74.7 us with all parts' first columns first, 71.9 so).
@@ -152,8 +162,11 @@ hipError_t launch_act_grad(const ActGradArgs& a, hipStream_t s) {
     else launch_kind<MOE_F16>(a, grid, per, shift, s);
     // many parts a slot: more lanes (63 parts of 2048 columns 3.4 us by 16 lanes, 5.9 by four; 128
     // slots of three parts on average 6.4 and 4.1)
-    if (a.dbias && parts > 8ll * S) act_grad_join_kernel<16><<<dim3(S, (N + 255) / 256), 1024, 0, s>>>(a.ws, (int)parts, N, a.dbias);
-    else if (a.dbias) act_grad_join_kernel<4><<<dim3(S, (N + 255) / 256), 256, 0, s>>>(a.ws, (int)parts, N, a.dbias);
+    int cols = lane_shift(N) + 1;  // lanes of four features, up to 64; fewer, down to 128 bytes, for eight workgroups
+    while (cols > 3 && (long long)S * ((N + (4 << cols) - 1) / (4 << cols)) < 8) --cols;
+    const dim3 join(S, (N + (4 << cols) - 1) / (4 << cols));
+    if (a.dbias && parts > 8ll * S) act_grad_join_kernel<1024><<<join, 1024, 0, s>>>(a.ws, (int)parts, N, cols, a.dbias);
+    else if (a.dbias) act_grad_join_kernel<256><<<join, 256, 0, s>>>(a.ws, (int)parts, N, cols, a.dbias);
     return hipGetLastError();
 }
 

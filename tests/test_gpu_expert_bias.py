@@ -252,6 +252,13 @@ def test_gradient_of_many_rows_and_slots():
     run_grad([40000, 0, 5], 256, BF, SWI, seed=10, h=False)
 
 
+@pytest.mark.parametrize("N", [8, 16, 24, 40, 64, 128, 136, 256, 264])
+@pytest.mark.parametrize("rows", [3, 600, 5000, 40000])
+def test_bias_gradient_of_narrow_rows(N, rows):
+    run_grad([rows], N, BF, Q.MOE_ACT_NONE, seed=N, dense=True)
+    run_grad([rows, 0, 7], N, F32, Q.MOE_ACT_RELU, seed=N, rows=PAIR, P=rows + 9, h=False)
+
+
 @pytest.mark.parametrize("kind", ACTS[1:])
 def test_gradient_far_out(kind):
     """Activations of values from 2^-100 to 2^100, both signs."""
