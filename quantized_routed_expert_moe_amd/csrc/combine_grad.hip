@@ -76,6 +76,7 @@ __global__ __launch_bounds__(512) void combine_grad_kernel(const CombineGradArgs
         float mine = 0.0f;
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
+            if (j >= n) continue;  // a sum over the lanes costs as much as a row of 512
             const float v = wave_sum(sum[j]);
             if (lane == j) mine = v;
         }
