@@ -652,7 +652,8 @@ moe_status moe_swiglu_backward(const void* gu, const void* dh, int dtype, int R,
  * slot_offsets, S, R, perm_pair, N  as for moe_expert_gemm (N a multiple of 8, SWIGLU
  *            of 16, N <= 2^20).
  * ws         device workspace of moe_expert_act_backward_workspace_size (0 for
- *            arguments out of range), 16-byte aligned; unused without dbias.
+ *            arguments out of range; never less for a larger S, N or R, so that one
+ *            of the largest serves all), 16-byte aligned; unused without dbias.
  * Sums over rows are taken in an order fixed by the sizes and offsets.
  */
 moe_status moe_expert_gemm_bias(const void* x, int dtype, const void* w, size_t w_stride, int S, int N, int K,

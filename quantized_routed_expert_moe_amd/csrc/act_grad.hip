@@ -7,6 +7,8 @@
 // second launch adds a slot's parts in order.  No atomics.  32768 rows of 768 of 128 slots (SwiGLU,
 // h again, bf16): 66 us of inputs from HBM (4.6 TB/s), 58 where the last-level cache holds half of
 // them, and 4 us for the sums.
+#include <algorithm>
+
 #include "act.h"
 #include "train_ops.h"
 
@@ -26,17 +28,25 @@ static int lane_shift(int n) {
 // 8192; 1001 rows of 2048 12 us in parts of 16 rows, 15 in 64), and for at most 1024 parts, which the
 // second launch adds (the sums alone of 16384 rows of 128: 23 us with 1024 parts and four columns a
 // lane for 256 of them, 10 so; 2^20 of 64: 96 with 4096 parts, 26 so, 5.2 TB/s).
+static int least_rows(int N) { return 2 * (256 >> lane_shift(N)); }
+static long long most_groups(int N, int R) {
+    const long long work = (long long)R * N / 16384;
+    return work < 512 ? 512 : work < 4096 ? work : 4096;
+}
 static int part_rows(int N, int R) {
-    const long long chunks = (N + 255) / 256, work = (long long)R * N / 16384;
-    const long long most = work < 512 ? 512 : work < 4096 ? work : 4096;
-    int per = 2 * (256 >> lane_shift(N));
+    const long long chunks = (N + 255) / 256, most = most_groups(N, R);
+    int per = least_rows(N);
     while (R / per > 1024 || R / per * chunks > most) per *= 2;
     return per;
 }
 static long long part_count(int S, int R, int per) { return (long long)R / per + (S < R ? S : R); }
 
+// The parts' number falls where their rows double, the need does not: it is what part_rows
+// allows.  With p = R / per, p N is at most R / least_rows N, 1024 N and 256 p chunks <= 256 most
+// (chunks is N / 256 rounded up), each of which grows with R and N.
 size_t act_grad_workspace_bytes(int S, int N, int R) {
-    return 4 * 1028 + (size_t)part_count(S, R, part_rows(N, R)) * N * sizeof(float);
+    const long long held = std::min({(long long)(R / least_rows(N)) * N, 1024ll * N, 256 * most_groups(N, R)});
+    return 4 * 1028 + (size_t)(held + (long long)std::min(S, R) * N) * sizeof(float);
 }
 
 // ACT 0: dz is dy, only the sums are wanted; 1: SwiGLU; 2: another activation.
