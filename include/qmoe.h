@@ -688,7 +688,7 @@ moe_status moe_expert_act_backward(const void* dy, const void* z, int dtype, int
  *            [2].  All of them are written: zeros for a sequence without rows, and
  *            losses of 0 for n = 0.
  * ws         device workspace of moe_balance_loss_workspace_size (0 for arguments
- *            out of range), 16-byte aligned.
+ *            out of range; never less for a larger T, E or G), 16-byte aligned.
  * Sums are fp32 in an order fixed by the sizes and offsets.
  *
  * moe_route_backward: the gradient of the logits,

@@ -14,6 +14,8 @@
 // s / sum s with s = t / (1 + t), t = e e^m: one exponential for both.  The latter is taken as
 // r / sum r with r = s for m >= 0 and r = e / (1 + t) = s e^-m for m < 0: rows of low
 // logits would underflow in s.
+#include <algorithm>
+
 #include "train_ops.h"
 
 namespace qmoe {
@@ -264,16 +266,18 @@ __global__ __launch_bounds__(1024) void loss_join_kernel(const RouterArgs a, con
 
 // Rows of a part: what a workgroup's waves hold at a time until there are 512 parts, of wide rows
 // 256 (4096 rows of 1024: 19.6 us in parts of 64, 14.4 in 16; 16384 of 1000: 24 in 64, 30 in 32).
+static int least_rows(int E) { return E <= 256 ? 64 : 16; }
+static int most_parts(int E) { return E <= 256 ? 512 : 256; }
 static int loss_rows(int T, int E) {
-    int per = E <= 256 ? 64 : 16;
-    while ((long long)T / per > (E <= 256 ? 512 : 256)) per *= 2;
+    int per = least_rows(E);
+    while (T / per > most_parts(E)) per *= 2;
     return per;
 }
 
-static LossParts loss_parts(int T, int E, int G, void* ws, size_t* bytes) {
+// whole: parts of `per` rows in all; beside them each sequence may begin one.
+static LossParts loss_parts(int whole, int T, int E, int G, void* ws, size_t* bytes) {
     LossParts l{};
-    l.per = loss_rows(T, E);
-    l.parts = T / l.per + (G < T ? G : T) + (T == 0);  // one at least: it writes the prefix
+    l.parts = whole + (G < T ? G : T) + (T == 0);  // one at least: it writes the prefix
     const size_t groups = (E + 63) / 64;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -291,10 +295,13 @@ static LossParts loss_parts(int T, int E, int G, void* ws, size_t* bytes) {
     return l;
 }
 
+// The parts' number falls where their rows double, and from 256 experts to 257; the need does
+// not: it is that of the most parts of any T up to this one, and for wide rows that of 256 experts at least.
 size_t balance_loss_workspace_bytes(int T, int E, int G) {
-    size_t bytes = 0;
-    loss_parts(T, E, G, nullptr, &bytes);
-    return bytes;
+    size_t bytes = 0, narrow = 0;
+    loss_parts(std::min(T / least_rows(E), most_parts(E)), T, E, G, nullptr, &bytes);
+    if (E > 256) loss_parts(std::min(T / least_rows(256), most_parts(256)), T, 256, G, nullptr, &narrow);
+    return std::max(bytes, narrow);
 }
 
 template <typename R>
@@ -329,7 +336,9 @@ static void by_width(int E, bool wide, F&& launch) {
 
 hipError_t launch_balance_loss(const RouterArgs& a, hipStream_t s) {
     const int G = a.seqs.S, groups = (a.E + 63) / 64;
-    const LossParts ws = loss_parts(a.T, a.E, G, a.ws, nullptr);
+    const int per = loss_rows(a.T, a.E);
+    LossParts ws = loss_parts(a.T / per, a.T, a.E, G, a.ws, nullptr);
+    ws.per = per;
     const bool alone = G == 1 && a.T <= 64;
     by_width(a.E, a.E % 4 == 0 && aligned16(a.logits), [&](auto row) { launch_loss_rows<decltype(row)>(a, ws, alone, s); });
     if (!alone) loss_join_kernel<<<dim3(G, groups), 1024, 0, s>>>(a, ws);

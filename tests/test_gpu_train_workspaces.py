@@ -29,3 +29,21 @@ def test_activation_gradient(small, large):
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     assert torch.equal(got[0][0], torch.where(z > 0, dy, torch.zeros_like(dy)))
     assert (behind == 0xA5).all()
+
+
+@pytest.mark.parametrize("E,small,large", [(256, 32831, 32832), (1000, 4111, 4112), (16, 100, 40000), (256, 300, 301)])
+def test_router_losses(E, small, large):
+    G, k = 8, 4
+    l = rand((small, E), F32, 1).cuda()
+    ids = torch.randint(0, E, (small, k), generator=torch.Generator().manual_seed(2), dtype=torch.int32).cuda()
+    off = torch.linspace(0, small, G + 1).int().cuda()
+    ws, behind = guarded(Q.moe_balance_loss_workspace_size(large, E, G))
+    roomy = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    got = []
+    for w in (ws, roomy):
+        counts = torch.zeros((G, E), dtype=torch.int32, device="cuda")
+        probs, losses = torch.zeros((G, E), device="cuda"), torch.zeros(2, device="cuda")
+        Q.moe_balance_loss(l, ids, Q.MOE_SCORE_SOFTMAX, counts, probs, losses, off, ws=w)
+        got.append((counts, probs, losses))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert int(got[0][0].sum()) == small * k and (behind == 0xA5).all()

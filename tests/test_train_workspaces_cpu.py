@@ -1,10 +1,10 @@
-"""The workspace query of the activations' gradient never falls where a size grows: one workspace for a program's largest
-batch serves every smaller one.  Without a GPU."""
+"""Workspace queries of the activations' gradient and of the router's losses never fall where a size grows: one workspace
+for a program's largest batch serves every smaller one.  Without a GPU."""
 import pytest
 
 import quantized_routed_expert_moe_amd as Q
 
-ACT = Q.moe_expert_act_backward_workspace_size
+ACT, LOSS = Q.moe_expert_act_backward_workspace_size, Q.moe_balance_loss_workspace_size
 TOP = 1 << 24
 
 
@@ -40,6 +40,20 @@ def test_activation_gradient_over_columns_and_slots(R):
         never_falls(lambda s: ACT(s, N, R), range(1, 1025))
 
 
+@pytest.mark.parametrize("E", [1, 8, 64, 256, 257, 512, 1000, 1024])
+@pytest.mark.parametrize("G", [1, 8, 1024])
+def test_router_losses_over_rows(E, G):
+    never_falls(lambda t: LOSS(t, E, G), around(TOP))
+
+
+@pytest.mark.parametrize("T", [0, 1, 64, 1039, 4111, 4112, 32831, 32832, TOP])
+def test_router_losses_over_experts_and_sequences(T):
+    for G in (1, 8, 1024):
+        never_falls(lambda e: LOSS(T, e, G), range(1, 1025))
+    for E in (16, 256, 257):
+        never_falls(lambda g: LOSS(T, E, g), range(1, 1025))
+
+
 def test_a_workspace_of_the_largest_batch_is_not_refused():
     """Past the size check of a smaller batch the next refusal is that of the address: nothing is enqueued."""
     fake = 1 << 20
@@ -49,3 +63,6 @@ def test_a_workspace_of_the_largest_batch_is_not_refused():
             st = Q.lib().moe_expert_act_backward(fake, fake * 2, Q.MOE_BF16, 1, 2048, None, small, None, 0, Q.MOE_ACT_GELU,
                                                  fake * 3, None, fake * 5, fake + 8, ws, None)
             assert st == want and needle in Q.lib().moe_last_error().decode(), (small, large)
+    for E, small, large in ((256, 32831, 32832), (1000, 4111, 4112)):
+        st = Q.lib().moe_balance_loss(fake, fake, small, E, 8, 0, fake, 8, fake, fake, fake, fake + 8, LOSS(large, E, 8), None)
+        assert st == Q.MOE_ERR_INVALID_ARGUMENT and "workspace must" in Q.lib().moe_last_error().decode(), (small, large)
