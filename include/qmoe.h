@@ -736,7 +736,8 @@ moe_status moe_combine_backward(const void* dy, int dy_dtype, const void* y_pair
  *         = |scale| * largest magnitude      (MOE_NORM_MAX; NaN if any is)
  *   outs[i] = grads[i] * scale * min(1, max_norm / (total + eps))
  * scale undoes a loss scale.  A total of infinity gives a factor of 0, one of
- * NaN a factor of NaN; where total + eps is 0 nothing is clipped.
+ * NaN a factor of NaN; where total + eps is 0 nothing is clipped, nor where max_norm is
+ * infinite, whatever the total (of finite gradients too it may lie beyond fp32), NaN aside.
  *
  * grads, counts, dtypes  host arrays of n: device addresses (aligned to their
  *            elements, any more is not needed), elements (0..2^40; NULL may stand for 0),

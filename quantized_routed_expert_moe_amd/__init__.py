@@ -943,7 +943,8 @@ def moe_grad_norm(grads, total, kind: int = MOE_NORM_L2, scale: float = 1.0, ws=
 
 
 def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float = 1.0, outs=None, stream=None):
-    """grads times scale min(1, max_norm / (total + eps)), in place or into outs (the same sizes, any of the types)."""
+    """grads times scale min(1, max_norm / (total + eps)), in place or into outs (the same sizes, any of the types);
+    max_norm = inf clips nothing."""
     dev = _op_device()
     lst = _op_list(grads, dev)
     _op_total(total)

@@ -255,8 +255,9 @@ __device__ __forceinline__ void clip_out(const L& t, int i, uint32_t c, uint32_t
 template <typename L>
 __global__ __launch_bounds__(256) void grad_clip_kernel(const L t, const float* total, float max_norm, float eps,
                                                         float scale) {
-    const double norm = (double)total[0] + (double)eps, limit = norm == 0.0 ? 1.0 : (double)max_norm / norm;
-    const float factor = (float)((double)scale * (limit > 1.0 ? 1.0 : limit));  // NaN stays
+    // a norm up to max_norm, infinities and 0 included, leaves a factor of 1; NaN stays
+    const double norm = (double)total[0] + (double)eps, limit = norm <= (double)max_norm ? 1.0 : (double)max_norm / norm;
+    const float factor = (float)((double)scale * limit);
     const uint32_t c = blockIdx.x;
     const int i = t.find(c);
     const uint32_t type = t.in_type(i), out = t.out_type(i);

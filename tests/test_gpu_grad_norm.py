@@ -235,6 +235,35 @@ def test_infinite_and_nan_totals():
     Q.moe_grad_clip(g, total, 1.0)
     assert torch.isnan(g[0]).all() and torch.isnan(g[1]).all()
 
+@pytest.mark.parametrize("kind", [BF, HF, F32])
+@pytest.mark.parametrize("place", ["in place", "another type", "odd place"])
+@pytest.mark.parametrize("total,max_norm,factor", [
+    (math.inf, math.inf, 1.0), (5.0, math.inf, 1.0), (0.0, math.inf, 1.0), (math.inf, 3.4028234663852886e38, 0.0),
+    (math.inf, 0.0, 0.0), (math.nan, math.inf, math.nan), (0.0, 0.0, 1.0),
+])
+def test_infinite_largest_norm_clips_nothing(kind, place, total, max_norm, factor):
+    """max_norm = inf leaves the gradients as they are whatever their total, NaN aside; scale still counts."""
+    for scale in (1.0, 0.5):
+        g = [rand((n,), kind, n).cuda() for n in (1, 1000, 4103)]
+        if place == "odd place":
+            g = [torch.cat((t[:1], t))[1:] for t in g]
+        first = [t.clone() for t in g]
+        outs = [torch.full(t.shape, -7.0, device="cuda") for t in g] if place == "another type" else None
+        Q.moe_grad_clip(g, torch.full((1,), total, device="cuda"), max_norm, 0.0, scale=scale, outs=outs)
+        for t, o in zip(first, outs or g):
+            want = t.to(o.dtype) * (scale * factor)  # a half, exactly, or one rounding of fp16's smallest
+            assert torch.equal(o, want) if factor == factor else torch.isnan(o).all()
+
+
+def test_overflowing_total_of_finite_gradients():
+    """The norm of finite gradients may lie beyond fp32: nothing is lost where no clipping is asked for."""
+    g = [torch.full((1000,), 3e38, device="cuda"), rand((5000,), F32, 1).cuda()]
+    first = [t.clone() for t in g]
+    total = norm(g)
+    assert float(total) == math.inf
+    Q.moe_grad_clip(g, total, math.inf)
+    assert all(torch.equal(a, b) for a, b in zip(first, g))
+
 
 def test_zero_gradients_stay_zero():
     g = [torch.zeros(100, device="cuda"), torch.zeros(9, dtype=BF, device="cuda")]
