@@ -641,6 +641,8 @@ moe_status moe_swiglu_backward(const void* gu, const void* dh, int dtype, int R,
  *   dbias_s[n]  = sum over q of slot s of dz[i(q), n]   (dz in fp32)
  * for the products' gradients, which take dz (moe_expert_gemm with transpose 1,
  * moe_expert_gemm_wgrad).  The residual's gradient is dy itself.
+ * An infinite z stands for a sum beyond dtype's range: dz and h are the limits there (act' is
+ * 0 or 1, silu 0 or infinite), and SwiGLU's products of 0 and an infinite half are 0.
  * dy         device, rows of N (SWIGLU: N / 2), dtype (any of the three).
  * z, dz      device, rows of N, dtype.  Both NULL for MOE_ACT_NONE (dz is dy).  dz may
  *            be z itself, and dy itself where the widths agree (in place).

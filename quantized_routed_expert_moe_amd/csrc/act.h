@@ -51,6 +51,10 @@ __device__ __forceinline__ void sigmoid_pair(float u, float& s, float& q) {
     q = u < 0.0f ? 1.0f - s : e * s;
 }
 
+// Gradients at an infinite z, which stands for a sum beyond its type's range (an fp16 sum past 65504 whose
+// activation was finite), are the limits there: the factors that vanish take z held within
+// act_range, of which finite z keep their bits.
+
 // dz = d act'(z), h = act(z).
 __device__ __forceinline__ void act_grad8(int act, const float* z, const float* d, float* dz, float* h) {
     if (act == MOE_ACT_SILU || act == MOE_ACT_GELU_TANH) {
@@ -62,7 +66,7 @@ __device__ __forceinline__ void act_grad8(int act, const float* z, const float* 
             float s, q;
             sigmoid_pair(c * fmaf(b * c, c, a), s, q);
             dz[i] = d[i] * (s * fmaf(c * q, fmaf(3.0f * b * c, c, a), 1.0f));
-            h[i] = z[i] * s;
+            h[i] = fmaxf(z[i], -1.0e4f) * s;  // NaN is in s
         }
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
@@ -70,8 +74,9 @@ __device__ __forceinline__ void act_grad8(int act, const float* z, const float* 
             const float p = 0.5f * (1.0f + erff(z[i] * 0.7071067811865476f));
             // z e^(-z^2 / 2) / sqrt(2 pi)
             const float t = -0.7213475204444817f * z[i] * z[i];
-            dz[i] = d[i] * fmaf(z[i], 0.3989422804014327f * __builtin_amdgcn_exp2f(t), p);
-            h[i] = z[i] * p;
+            const float c = __builtin_amdgcn_fmed3f(z[i], -1.0e4f, 1.0e4f);
+            dz[i] = d[i] * fmaf(c, 0.3989422804014327f * __builtin_amdgcn_exp2f(t), p);  // NaN is in p
+            h[i] = fmaxf(z[i], -1.0e4f) * p;
         }
     } else {
 #pragma unroll
@@ -80,6 +85,26 @@ __device__ __forceinline__ void act_grad8(int act, const float* z, const float* 
             h[i] = z[i] < 0.0f ? 0.0f : z[i];
         }
     }
+}
+
+// a v, 0 for a = 0 and infinite v.
+__device__ __forceinline__ float times_limit(float a, float v) { return a == 0.0f && __builtin_isinf(v) ? 0.0f : a * v; }
+
+// SwiGLU of g and u and its gradient for given d.
+__device__ __forceinline__ void swiglu_grad(float g, float u, float d, float& dg, float& du, float& h) {
+    const float s = sigmoid_f32(g);
+    h = g * s * u;
+    dg = d * u * s * (1.0f + g * (1.0f - s));
+    du = d * g * s;
+}
+
+// The same where g or u may be infinite.
+__device__ __forceinline__ void swiglu_grad_limit(float g, float u, float d, float& dg, float& du, float& h) {
+    if (!__builtin_isinf(g) && !__builtin_isinf(u)) return swiglu_grad(g, u, d, dg, du, h);
+    const float c = act_range(g), s = sigmoid_f32(c), gs = fmaxf(g, -1.0e4f) * s;
+    h = __builtin_isinf(gs) ? times_limit(u, gs) : times_limit(gs, u);
+    dg = times_limit(d * (s * (1.0f + c * (1.0f - s))), u);
+    du = times_limit(d, gs);
 }
 
 }  // namespace qmoe

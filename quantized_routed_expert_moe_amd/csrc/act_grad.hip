@@ -49,6 +49,36 @@ size_t act_grad_workspace_bytes(int S, int N, int R) {
     return 4 * 1028 + (size_t)(held + (long long)std::min(S, R) * N) * sizeof(float);
 }
 
+// Eight elements in their own type, and acc, made NaN if one of them is infinite or NaN (0 v is NaN then):
+// an instruction for each two 16-bit ones, which stay packed.
+template <int DT> using Vec8 __attribute__((ext_vector_type(8))) = typename DType<DT>::type;
+template <int DT>
+__device__ __forceinline__ Vec8<DT> load_as(const void* base, size_t at) {
+    typedef Vec8<DT> vec __attribute__((aligned(16)));
+    return *reinterpret_cast<const vec*>(static_cast<const typename DType<DT>::type*>(base) + at);
+}
+template <int DT>
+__device__ __forceinline__ float not_finite(Vec8<DT> v, float acc) {
+    typedef typename DType<DT>::type pair __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        if constexpr (DT == MOE_F32) acc = fmaf(0.0f, v[i], fmaf(0.0f, v[i + 1], acc));
+        else if constexpr (DT == MOE_BF16) acc = __builtin_amdgcn_fdot2_f32_bf16(pair{v[i], v[i + 1]}, pair{0, 0}, acc, false);
+        else acc = __builtin_amdgcn_fdot2(pair{v[i], v[i + 1]}, pair{0, 0}, acc, false);
+    }
+    return acc;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const void* p, size_t at) {
+    return (float)static_cast<const typename DType<DT>::type*>(p)[at];
+}
+template <int DT>
+__device__ __forceinline__ void store_one(void* p, size_t at, float v) {
+    typedef typename DType<DT>::type E;
+    static_cast<E*>(p)[at] = (E)v;
+}
+
 // ACT 0: dz is dy, only the sums are wanted; 1: SwiGLU; 2: another activation.
 // A row has 2^cl_shift lanes of eight features.
 template <int DT, int KIND>
@@ -67,35 +97,56 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, int 
     if (in)
         for (int r0 = threadIdx.x >> cl_shift; r0 < nq; r0 += kRows * rl) {
             size_t row[kRows];
-            float d[kRows][8], z[kRows][8], u[kRows][8];
+            Vec8<DT> zr[kRows], ur[kRows], dr[kRows];
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
                 const int r = r0 + j * rl;
                 if (r >= nq) continue;
                 row[j] = row_of(a.rows, a.how, q0 + r);
-                if (KIND) load_vec8<DT>(a.z, row[j] * N + c, z[j]);
-                if (KIND == 1) load_vec8<DT>(a.z, row[j] * N + I + c, u[j]);
-                load_vec8<DT>(a.dy, row[j] * I + c, d[j]);
+                if (KIND) zr[j] = load_as<DT>(a.z, row[j] * N + c);
+                if (KIND == 1) ur[j] = load_as<DT>(a.z, row[j] * N + I + c);
+                dr[j] = load_as<DT>(a.dy, row[j] * I + c);
             }
 #pragma unroll
             for (int j = 0; j < kRows; ++j) {
                 if (r0 + j * rl >= nq) continue;
-                float dz[8], du[8], h[8];
+                if (KIND == 1 && __any(not_finite<DT>(zr[j], not_finite<DT>(ur[j], 0.0f)) != 0.0f)) {
+                    // one element at a time, loaded again: registers are what the loop is short of
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        float dg, du, h;
+                        swiglu_grad_limit(load_one<DT>(a.z, row[j] * N + c + i), load_one<DT>(a.z, row[j] * N + I + c + i),
+                                          load_one<DT>(a.dy, row[j] * I + c + i), dg, du, h);
+                        store_one<DT>(a.dz, row[j] * N + c + i, dg);
+                        store_one<DT>(a.dz, row[j] * N + I + c + i, du);
+                        if (a.h) store_one<DT>(a.h, row[j] * I + c + i, h);
+#pragma unroll
+                        for (int t = 0; t < 8; ++t) {
+                            sum[t] += t == i ? dg : 0.0f;
+                            sum[8 % W + t] += t == i ? du : 0.0f;
+                        }
+                    }
+                    continue;
+                }
+                float z[8], u[8], d[8], dz[8], du[8], h[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (KIND == 1) {
-                        const float g = z[j][i], s = sigmoid_f32(g);
-                        h[i] = g * s * u[j][i];
-                        dz[i] = d[j][i] * u[j][i] * s * (1.0f + g * (1.0f - s));
-                        du[i] = d[j][i] * g * s;
-                        sum[8 % W + i] += du[i];
-                    } else {
-                        dz[i] = d[j][i];
-                    }
+                    if (KIND) z[i] = (float)zr[j][i];
+                    if (KIND == 1) u[i] = (float)ur[j][i];
+                    d[i] = (float)dr[j][i];
                 }
-                if (KIND == 2) act_grad8(a.act, z[j], d[j], dz, h);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] += dz[i];
+                for (int i = 0; i < 8; ++i) {
+                    if (KIND == 1) swiglu_grad(z[i], u[i], d[i], dz[i], du[i], h[i]);
+                    if (KIND == 0) dz[i] = d[i];
+                }
+                if (KIND == 2) act_grad8(a.act, z, d, dz, h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+#pragma clang fp contract(off)  // the same sums wherever the compiler puts the products
+                    sum[i] += dz[i];
+                    if (KIND == 1) sum[8 % W + i] += du[i];
+                }
                 if (KIND) {
                     store_vec8<DT>(a.dz, row[j] * N + c, dz);
                     if (KIND == 1) store_vec8<DT>(a.dz, row[j] * N + I + c, du);

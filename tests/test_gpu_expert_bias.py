@@ -1,5 +1,7 @@
 """moe_expert_gemm_bias and moe_expert_act_backward against their formulas in 64 bits: activations, types, row modes,
 ragged and empty slots, both kinds of product kernels, in-place forms, and the gradients against differences."""
+import math
+
 import pytest
 import torch
 
@@ -275,6 +277,81 @@ def test_gradient_far_out(kind):
     bound = torch.cat((16 * F + 0 * own, own), 1) if kind == SWI else own
     within(dz, wd, bound, "dz")
     within(h, act(zd, kind), 8 * F * zd[:, :8].abs(), "h")
+
+INF = math.inf
+
+
+def limits(kind, z, d):
+    """act and d act' at infinite z as their limits (SwiGLU: z = (g, u)): a factor of 0 stays 0.  A sigmoid below fp32's
+    range (of less than -104) is one."""
+    times = lambda a, v: 0.0 if a == 0 and math.isinf(v) else a * v
+    if kind == SWI:
+        g, u = z
+        s = 0.0 if g < -104 else 1.0 if g == INF else 1 / (1 + math.exp(-g))
+        gs = 0.0 if g == -INF else g * s
+        slope = s if math.isinf(g) else s * (1 + g * (1 - s))
+        h = times(u, gs) if math.isinf(gs) else times(gs, u)
+        return h, (times(d * slope, u), times(d, gs))
+    return (INF, (d,)) if z > 0 else (0.0, (0.0 * d,))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, F32])
+@pytest.mark.parametrize("kind", ACTS[1:])
+def test_gradient_of_infinite_sums(kind, dtype):
+    """z beyond its type's range is stored as infinite: gradients are the limits there, not NaN; NaN stays NaN."""
+    if kind == SWI:
+        cases = [(g, u, d) for g in (INF, -INF, 0.0, 1.5, -2.0, -200.0) for u in (INF, -INF, 0.0, 2.0, -3.0)
+                 for d in (0.0, 1.0, -0.5) if math.isinf(g) or math.isinf(u)]
+    else:
+        cases = [(z, d) for z in (INF, -INF) for d in (0.0, 1.0, -0.5)]
+    n = -(-len(cases) // 8) * 8
+    cases = (cases * 8)[:n]
+    want = [limits(kind, c[:2] if kind == SWI else c[0], c[-1]) for c in cases]
+    z = torch.tensor([c[0] for c in cases] + ([c[1] for c in cases] if kind == SWI else []), dtype=dtype)[None]
+    dy = torch.tensor([c[-1] for c in cases], dtype=dtype)[None]
+    dz, h = torch.empty_like(z, device="cuda"), torch.empty_like(dy, device="cuda")
+    db = torch.empty((1, z.shape[1]), device="cuda")
+    ws = torch.empty(Q.moe_expert_act_backward_workspace_size(1, z.shape[1], 1), dtype=torch.uint8, device="cuda")
+    Q.moe_expert_act_backward(dy.cuda(), z.cuda(), None, dz, db, act=kind, h=h, ws=ws)
+    wd = torch.tensor([w[1][i] for i in range(2 if kind == SWI else 1) for w in want], dtype=D)[None]
+    wh = torch.tensor([w[0] for w in want], dtype=D)[None]
+    # finite ones: the sigmoid's and four products' roundings of values below 10
+    within(dz, wd, 100 * F + store_bound(wd.nan_to_num(posinf=0, neginf=0), dtype), "dz")
+    within(db, wd, torch.full_like(wd, 100 * F), "dbias")
+    within(h, wh, 100 * F + store_bound(wh.nan_to_num(posinf=0, neginf=0), dtype), "h")
+    z = torch.full_like(z, math.nan)
+    Q.moe_expert_act_backward(dy.cuda(), z.cuda(), None, dz, None, act=kind, h=h)
+    if kind != Q.MOE_ACT_RELU:
+        assert torch.isnan(dz).all()
+    assert torch.isnan(h).all()
+
+
+@pytest.mark.parametrize("kind", ACTS[1:])
+def test_gradient_where_fp16_sums_overflow(kind):
+    """The product's own fp16 z is infinite where the sums pass 65504; y in fp32 is finite, and so is what the gradient
+    makes of it where it has a limit.  The elements beside the infinite ones keep their bits."""
+    N, K, R = 32, 16, 24
+    x, w = torch.full((R, K), 200.0, dtype=HF), rand((1, N, K), HF, 1)
+    w[:, 3], w[:, 7], w[:, 20] = 30.0, -30.0, 25.0  # sums of +-96000 and 80000
+    I = N // 2 if kind == SWI else N
+    y, z = torch.empty((R, I), device="cuda"), torch.empty((R, N), dtype=HF, device="cuda")
+    Q.moe_expert_gemm_bias(x.cuda(), w.cuda(), None, None, None, y, act=kind, z=z)
+    assert torch.isfinite(y).all() and (z[:, 3] == INF).all() and (z[:, 7] == -INF).all() and (z[:, 20] == INF).all()
+    dy = rand((R, I), HF, 2).abs()  # of one sign: so are the infinite terms of a bias's gradient
+    dy[::3] = 0
+    dz, h, db = torch.empty_like(z), torch.empty((R, I), dtype=HF, device="cuda"), torch.empty((1, N), device="cuda")
+    ws = torch.empty(Q.moe_expert_act_backward_workspace_size(1, N, R), dtype=torch.uint8, device="cuda")
+    Q.moe_expert_act_backward(dy.cuda(), z, None, dz, db, act=kind, h=h, ws=ws)
+    assert not torch.isnan(dz).any() and not torch.isnan(h).any() and not torch.isnan(db).any()
+    assert (dz[::3] == 0).all()
+    others = z.clone()
+    others[torch.isinf(z)] = 1.0
+    dz2, h2 = torch.empty_like(z), torch.empty_like(h)
+    Q.moe_expert_act_backward(dy.cuda(), others, None, dz2, None, act=kind, h=h2)
+    far = torch.isinf(z)
+    if kind == SWI:
+        far = (far[:, :I] | far[:, I:]).repeat(1, 2)
+    assert torch.equal(dz[~far], dz2[~far]) and torch.equal(h[~far[:, :I]], h2[~far[:, :I]])
 
 
 @pytest.mark.parametrize("kind", ACTS[1:])
