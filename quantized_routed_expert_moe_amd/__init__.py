@@ -540,6 +540,16 @@ def _op_matrix(t, cols: int, R: int, mode: int, k: int, name: str) -> None:
         raise ValueError(f"{name} has shape {tuple(shape)}, expected at least {need} rows of {cols}")
 
 
+def _op_width(N: int, act: int) -> int:
+    """Outputs of a product without an epilogue."""
+    if act == MOE_ACT_NONE:
+        return N
+    if act != MOE_ACT_SWIGLU:
+        raise QmoeError(MOE_ERR_INVALID_ARGUMENT, f"act {act} is neither MOE_ACT_NONE nor MOE_ACT_SWIGLU "
+                        "(moe_expert_gemm_bias takes the others)")
+    return N // 2
+
+
 def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: int = MOE_ROWS_POSITION,
                     y_rows: int = MOE_ROWS_POSITION, transpose: bool = False, act: int = MOE_ACT_NONE, stream=None):
     """y rows = x rows times their slot's matrix of w [S, N, K] (transposed unless `transpose`)."""
@@ -548,7 +558,7 @@ def moe_expert_gemm(x, w, slot_offsets, y, perm_pair=None, k: int = 1, x_rows: i
     if len(shape) != 3 or strides[2] != 1 or (strides[1] != shape[2] and shape[1] != 1):
         raise ValueError("w must be [S, N, K] with contiguous matrices")
     S, N, K = shape
-    wide_in, wide_out = (N, K) if transpose else (K, N // 2 if act else N)
+    wide_in, wide_out = (N, K) if transpose else (K, _op_width(N, act))
     R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
     _op_matrix(x, wide_in, R, x_rows, k, "x")
     _op_matrix(y, wide_out, R, y_rows, k, "y")
@@ -600,7 +610,7 @@ def moe_expert_gemv_w4(x, q, scales, zeros, group: int, slot_offsets, y, perm_pa
         raise ValueError("zeros must be uint8 with the shape of scales")
     R = _op_rows(slot_offsets, S, perm_pair, x, (x_rows, y_rows), k)
     _op_matrix(x, K, R, x_rows, k, "x")
-    _op_matrix(y, N // 2 if act else N, R, y_rows, k, "y")
+    _op_matrix(y, _op_width(N, act), R, y_rows, k, "y")
     xp, qp, sp, zp, op, pp, yp = _op_ptrs(dev, "x q scales zeros slot_offsets perm_pair y", x, q, scales, zeros,
                                           slot_offsets, perm_pair, y)
     _check(lib().moe_expert_gemv_w4(xp, _op_code(x, "x"), qp, sp, _op_code(scales, "scales"), zp, group, S, N, K, op,

@@ -39,7 +39,9 @@ moe_status check_product(int dtype, int S, int N, int K, const int32_t* slot_off
     if (N <= 0 || K <= 0) return fail(MOE_ERR_INVALID_ARGUMENT, "N = %d, K = %d must be positive", N, K);
     if (N % 8 || K % 8) return fail(MOE_ERR_UNSUPPORTED, "N = %d and K = %d must be multiples of 8", N, K);
     if ((long long)N * K > kMaxMatrix) return fail(MOE_ERR_UNSUPPORTED, "N*K = %lld exceeds 2^30", (long long)N * K);
-    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU) return fail(MOE_ERR_INVALID_ARGUMENT, "bad act %d", act);
+    if (act != MOE_ACT_NONE && act != MOE_ACT_SWIGLU)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "act %d is neither MOE_ACT_NONE nor MOE_ACT_SWIGLU (moe_expert_gemm_bias takes the others)",
+                    act);
     if (act == MOE_ACT_SWIGLU && N % 16)
         return fail(MOE_ERR_UNSUPPORTED, "MOE_ACT_SWIGLU needs N (%d) a multiple of 16", N);
     if (R < 0 || R > kMaxRows) return fail(MOE_ERR_INVALID_ARGUMENT, "R = %d outside 0..2^24", R);
