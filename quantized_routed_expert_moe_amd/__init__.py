@@ -12,6 +12,7 @@ import bisect
 import ctypes
 import os
 import re
+import weakref
 
 import numpy as np
 
@@ -963,7 +964,7 @@ def moe_grad_clip(grads, total, max_norm: float, eps: float = 1e-6, scale: float
     op = oc = ot = None
     if outs is not None:
         out = _op_list(outs, dev)
-        if lst.apart is not out:
+        if lst.apart is None or lst.apart() is not out:
             _op_apart(lst, out)
         op, oc, ot = out.c_at, out.c_codes, out.table_on(stream)
     _check(lib().moe_grad_clip(lst.c_at, lst.c_counts, lst.c_codes, lst.n, lst.table_on(stream), op, oc, ot, tp,
@@ -985,7 +986,7 @@ def _op_apart(lst: _TensorList, out: _TensorList) -> None:
         j = bisect.bisect_left(starts, a + c * (4 if code == MOE_F32 else 2))
         if j and lst.ranges[j - 1][1] > a:
             raise ValueError("an output overlaps another gradient")
-    lst.apart = out
+    lst.apart = weakref.ref(out)  # the outputs' memory is their owner's
 
 
 # ------------------------------------------------------------ host leg
