@@ -331,6 +331,37 @@ def test_offsets_that_decrease_stay_in_bounds():
         assert d.shape == l.shape
 
 
+def inside(shape, dtype, mark):
+    """A tensor in the middle of a marked buffer, on a 16-byte boundary, and the check of what lies around it."""
+    n = math.prod(shape) * torch.empty((), dtype=dtype).element_size()
+    whole = torch.full((4096 + n + 4096,), mark, dtype=torch.uint8, device="cuda")
+    t = whole[4096:4096 + n].view(dtype).reshape(shape)
+    return t, lambda: bool((whole[:4096] == mark).all() and (whole[4096 + n:] == mark).all())
+
+
+@pytest.mark.parametrize("T,E", [(300, 16), (37, 16), (1000, 264), (300, 30)])
+@pytest.mark.parametrize("score", [SOFT, SIGM])
+def test_offsets_that_decrease_leave_what_lies_around(T, E, score):
+    """As above, with marked memory on both sides of everything that the calls write, the workspace of its exact size."""
+    l, ids = batch(T, E, 2, 1)
+    l, ids, dw, ones = l.cuda(), ids.cuda(), torch.ones((T, 2), device="cuda"), torch.ones(2, device="cuda")
+    for bounds in ([0, T, 0, T, 0, T], [T, 0], [-5, T + 700], [2 ** 31 - 1, -2 ** 31, 7], [T] * 9 + [0], list(range(T, -1, -1))):
+        G, off = len(bounds) - 1, torch.tensor(bounds, dtype=torch.int32, device="cuda")
+        counts, c = inside((G, E), torch.int32, 0x5A)
+        probs, p = inside((G, E), F32, 0x5A)
+        losses, o = inside((2,), F32, 0x5A)
+        ws, w = inside((Q.moe_balance_loss_workspace_size(T, E, G),), torch.uint8, 0x5A)
+        grads = [inside((T, E), t, 0x5A) for t in (F32, BF)]
+        Q.moe_balance_loss(l, ids, score, counts, probs, losses, off, ws=ws)
+        for d, _ in grads:
+            Q.moe_route_backward(l, ids, dw, score, True, 1.0, counts, ones, off, d)
+        torch.cuda.synchronize()
+        assert c() and p() and o() and w() and all(check() for _, check in grads), bounds
+        # whatever the values, all of them are written (the mark is 1.5e16 in both types)
+        for t in (counts, probs, losses, grads[0][0], grads[1][0]):
+            assert not (t == torch.full((16,), 0x5A, dtype=torch.uint8, device="cuda").view(t.dtype)[0]).any(), bounds
+
+
 def test_binding_refuses():
     l, ids = batch(6, 16, 2, 1)
     l, ids = l.cuda(), ids.cuda()
