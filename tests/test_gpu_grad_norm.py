@@ -129,6 +129,36 @@ def test_long_list_captured_outlives_its_table():
     assert int(fill[0]) == 255
 
 
+def test_long_list_captured_does_not_read_its_table():
+    """The tables' own bytes are cleared before the replays: entries of nothing, with which a norm would be 0 and outputs
+    would stay."""
+    grads = [rand((100 + i,), F32, i).cuda() for i in range(300)]
+    total, ws = torch.zeros(1, device="cuda"), torch.empty(Q.moe_grad_norm_workspace_size(300), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(g) for g in grads]
+    lst, out = Q.moe_tensor_list(grads), Q.moe_tensor_list(outs)
+    Q.moe_grad_norm(lst, total, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        Q.moe_grad_norm(lst, total, ws=ws)
+        Q.moe_grad_clip(lst, total, 2.0, outs=out)
+    for t in (lst.table, out.table):
+        t.zero_()
+    torch.cuda.synchronize()
+    for seed in range(3):
+        for g, o in zip(grads, outs):
+            g.copy_(rand(g.shape, F32, seed * 1000 + g.numel()))
+            o.fill_(-7.0)
+        total.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = exact(grads)
+        assert abs(float(total) - want) <= F * want * 1.001
+        for g, o in zip(grads, outs):
+            w = g.cpu().to(D) * min(1.0, 2.0 / (want + 1e-6))
+            within(o, w, 3 * F * w.abs() * 1.001, "clipped")
+
+
 def test_empty_lists_and_tensors():
     assert float(norm([])) == 0.0
     empty = [torch.empty(0, dtype=BF, device="cuda"), torch.empty((0, 5), device="cuda")]
