@@ -5,8 +5,8 @@
 // slot and a run of columns; a thread takes eight columns through every rl-th
 // row and holds their sums, which the workgroup joins and stores as one part; a
 // second launch adds a slot's parts in order.  No atomics.  32768 rows of 768 of 128 slots (SwiGLU,
-// h again, bf16): 66 us of inputs from HBM (4.6 TB/s), 58 where the last-level cache holds half of
-// them, and 4 us for the sums.
+// h again, bf16): 67 us of inputs from HBM (4.5 TB/s) and 4 us for the sums.  A wave's test for infinite
+// halves is 1 % of it (66.4 and 67.2 us).
 #include <algorithm>
 
 #include "act.h"
@@ -49,14 +49,14 @@ size_t act_grad_workspace_bytes(int S, int N, int R) {
     return 4 * 1028 + (size_t)(held + (long long)std::min(S, R) * N) * sizeof(float);
 }
 
-// Eight elements in their own type, and acc, made NaN if one of them is infinite or NaN (0 v is NaN then):
-// an instruction for each two 16-bit ones, which stay packed.
+// Eight elements in their own type: 16-bit ones stay packed until they are used.
 template <int DT> using Vec8 __attribute__((ext_vector_type(8))) = typename DType<DT>::type;
 template <int DT>
 __device__ __forceinline__ Vec8<DT> load_as(const void* base, size_t at) {
     typedef Vec8<DT> vec __attribute__((aligned(16)));
     return *reinterpret_cast<const vec*>(static_cast<const typename DType<DT>::type*>(base) + at);
 }
+// acc, made NaN if an element is infinite or NaN (0 v is NaN then).
 template <int DT>
 __device__ __forceinline__ float not_finite(Vec8<DT> v, float acc) {
     typedef typename DType<DT>::type pair __attribute__((ext_vector_type(2)));
@@ -79,7 +79,7 @@ __device__ __forceinline__ void store_one(void* p, size_t at, float v) {
     static_cast<E*>(p)[at] = (E)v;
 }
 
-// ACT 0: dz is dy, only the sums are wanted; 1: SwiGLU; 2: another activation.
+// KIND 0: dz is dy, only the sums are wanted; 1: SwiGLU; 2: another activation.
 // A row has 2^cl_shift lanes of eight features.
 template <int DT, int KIND>
 __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a, int per, int cl_shift) {
